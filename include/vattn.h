@@ -97,8 +97,9 @@ enum {
 };
 
 /* bits of the device error word; VATTN_DEV_TIMEOUT: a kernel's bounded wait
-   for its own copies ran out, so the call's outputs are not valid */
-enum { VATTN_DEV_BAD_SEQLEN = 1, VATTN_DEV_BAD_PAGE = 2, VATTN_DEV_TIMEOUT = 4 };
+   for its own copies ran out, so the call's outputs are not valid;
+   VATTN_DEV_BAD_GROUP: the groups of a shared-prefix decode are not valid */
+enum { VATTN_DEV_BAD_SEQLEN = 1, VATTN_DEV_BAD_PAGE = 2, VATTN_DEV_TIMEOUT = 4, VATTN_DEV_BAD_GROUP = 8 };
 
 typedef struct vattn_ctx vattn_ctx;
 
@@ -212,6 +213,145 @@ int vattn_dense_decode_static(const vattn_config* cfg, const void* q, const void
                               const void* v_cache, const int32_t* page_table,
                               const int32_t* seq_lens, int batch, int num_pages, float* out,
                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * A rotation plan turns the first rot_dim components of a head, as rot_dim / 2
+ * pairs (x_a, x_b): (i, i + rot_dim / 2) in the half layout, (2i, 2i + 1) in
+ * the interleaved one. At position p, with angle p * f_i and amplitude A,
+ *   y_a = A (x_a cos - x_b sin),   y_b = A (x_b cos + x_a sin);
+ * the components from rot_dim on are copied. f_i starts as base^(-2i/rot_dim)
+ * and is scaled for contexts longer than the original one by:
+ *   LINEAR  f_i / factor;
+ *   BASE    the base times factor^(rot_dim / (rot_dim - 2)) (rot_dim = 2: none);
+ *   BANDS   with t = original_ctx * f_i / 2 pi turns: f_i / factor below `low`
+ *           turns, f_i above `high`, in between weighted (t - low) / (high - low);
+ *   YARN    from f_i to f_i / factor along a ramp over the pair index i, from
+ *           max(floor(c(fast)), 0) to min(ceil(c(slow)), rot_dim - 1) (at least
+ *           0.001 long), c(n) = rot_dim ln(original_ctx / (2 pi n)) / (2 ln base);
+ *           the amplitude defaults to 0.1 ln(factor) + 1 (factor > 1).
+ * Angles are exact to 2^-32 of a turn at every 32-bit position (negative ones
+ * included): the plan holds f_i / 2 pi as 64-bit fractions of a turn, whose
+ * product with the position wraps by itself. The arithmetic is fp32, rounded
+ * once to the element type. */
+enum { VATTN_ROPE_HALF = 0, VATTN_ROPE_INTERLEAVED = 1 };
+enum {
+  VATTN_ROPE_NONE = 0,
+  VATTN_ROPE_LINEAR = 1,
+  VATTN_ROPE_BASE = 2,
+  VATTN_ROPE_BANDS = 3,
+  VATTN_ROPE_YARN = 4
+};
+
+typedef struct {
+  int head_dim;        /* 64 or 128                                              */
+  int rot_dim;         /* even, in [2, head_dim]                                 */
+  int layout;          /* VATTN_ROPE_HALF or VATTN_ROPE_INTERLEAVED              */
+  int scaling;         /* VATTN_ROPE_*                                           */
+  double base;         /* > 1                                                    */
+  double factor;       /* > 0 (LINEAR, BASE, BANDS, YARN)                        */
+  double original_ctx; /* > 0 (BANDS, YARN)                                      */
+  double low, high;    /* 0 < low < high (BANDS)                                 */
+  double slow, fast;   /* 0 < slow < fast (YARN): turns over original_ctx        */
+  double amplitude;    /* > 0, or 0 for the scaling's own (1, or YARN's formula) */
+} vattn_rope_config;
+
+/* A plan: host data only, filled by vattn_rope_init, copied into each launch. */
+typedef struct {
+  int head_dim, rot_dim, layout;
+  float amplitude;
+  uint64_t turns[64]; /* f_i / 2 pi in units of 2^-64 of a turn */
+} vattn_rope;
+
+/* Fills *rope from *cfg. Touches no device. VATTN_EINVAL for a bad field. */
+int vattn_rope_init(vattn_rope* rope, const vattn_rope_config* cfg);
+
+/* out = x rotated to `positions`, on the current device, without a context.
+     x, out     [tokens][heads][head_dim] `dtype` with the given strides in
+                elements (the components of a head are contiguous)
+     positions  [tokens] int32, any value
+   transpose != 0 applies the transposed map instead (angles negated, the same
+   amplitude): the gradient of x from the gradient of out. out may be x itself
+   with x's strides; otherwise no element of out may be one of x. tokens = 0
+   or heads = 0 does nothing. VATTN_EINVAL for a plan that vattn_rope_init did
+   not fill, a null pointer, negative sizes or strides, more than 2^30 tokens or
+   2^16 heads, or a stride of out
+   that would make two heads or tokens overlap (smaller than a head, or than
+   all heads of a token). */
+int vattn_rotate(const vattn_rope* rope, const void* x, void* out, const int32_t* positions,
+                 int tokens, int heads, int dtype, long long x_token_stride,
+                 long long x_head_stride, long long out_token_stride, long long out_head_stride,
+                 int transpose, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Appending to the cache: the writer of what vattn_decode reads.
+ *
+ * `tokens` new tokens, packed sequence by sequence: sequence b owns rows
+ * cu_tokens[b] .. cu_tokens[b + 1] - 1 of k, v and q, n_b of them. seq_lens
+ * counts the new tokens already, so the same array serves the decode that
+ * follows: row cu_tokens[b] + i has position seq_lens[b] - n_b + i, and goes to
+ * the slot that page_table gives that position. cu_tokens = NULL is the decode
+ * form: one token per sequence (tokens == batch) at position seq_lens[b] - 1; a
+ * sequence of length 0 appends nothing.
+ * Per token: k_cache gets the key rotated by `rope`, v_cache the value; a
+ * SparQ context's k_t_cache the same key dim-major; a Loki context's
+ * k_proj_cache the stored (rounded) key times the basis, summed in fp32; q_out
+ * the rotated query. Nothing else of the caches or of q_out is written: rows
+ * from cu_tokens[batch] on are left alone.
+ * Slots must differ: two tokens with one slot (a page listed twice) race.
+ * Device-side violations never trap: a sequence with n_b < 0, rows outside
+ * [0, tokens), seq_lens[b] < n_b or seq_lens[b] > max_ctx sets
+ * VATTN_DEV_BAD_SEQLEN and is skipped; a token whose page id is out of range sets
+ * VATTN_DEV_BAD_PAGE and is skipped (its q_out row too). */
+typedef struct {
+  const vattn_rope* rope;   /* host; NULL: k and q are taken as they are          */
+  int tokens;               /* rows of k, v and q, 0 to 2^30                      */
+  int num_pages;            /* as in vattn_params                                 */
+  const int32_t* cu_tokens; /* [batch + 1] device, or NULL (tokens == batch)      */
+  const void* k;            /* [tokens][Hkv][d], k_stride elements per token      */
+  const void* v;            /* [tokens][Hkv][d], v_stride elements per token      */
+  const void* q;            /* [tokens][Hq][d], q_stride elements per token, or   */
+                            /* NULL                                               */
+  long long k_stride, v_stride, q_stride; /* >= the heads of a token             */
+  void* q_out;              /* [tokens][Hq][d] contiguous; required with q. May   */
+                            /* be q itself when q is contiguous, else disjoint    */
+  void* k_cache;
+  void* v_cache;
+  void* k_t_cache;          /* SparQ context: required; else ignored              */
+  void* k_proj_cache;       /* Loki context: required, with proj_basis; else      */
+  const float* proj_basis;  /* ignored                                            */
+} vattn_append_params;
+
+/* Enqueued on `stream` of the context's device (whichever device is current),
+   one launch, no workspace, so calls on one context may overlap. Host-resident
+   caches (VATTN_KV_HOST) are written over the host link. */
+int vattn_append(vattn_ctx* ctx, const vattn_append_params* params, const int32_t* page_table,
+                 const int32_t* seq_lens, int batch, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Dense decode for a batch that shares prefixes: vattn_dense_decode's result,
+ * with every shared prefix's keys and values read once per group of sequences.
+ *   group_start  [groups + 1] device int32, ascending from 0 to batch: group g
+ *                is sequences group_start[g] .. group_start[g + 1] - 1
+ *   prefix_lens  [groups] device int32, in [0, max_ctx]: positions
+ *                0 .. prefix_lens[g] - 1 hold the same keys and values in every
+ *                sequence of the group. They are read through the page table of
+ *                the group's first sequence (which has to list them even if that
+ *                sequence itself is shorter), the rest through each
+ *                sequence's own. The prefix need not end on a page.
+ * A sequence shorter than its group's prefix is decoded by itself from its own
+ * pages. An empty sequence gives a zero output. Invalid groups (not ascending
+ * from 0 to batch, a prefix outside [0, max_ctx]) set VATTN_DEV_BAD_GROUP, and
+ * a prefix page out of range VATTN_DEV_BAD_PAGE: the sequences of such a group,
+ * and those in no group, give a zero output.
+ * Uses the context's workspace like the other decodes: order the calls of one
+ * context. */
+int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const void* k_cache,
+                              const void* v_cache, const int32_t* page_table,
+                              const int32_t* seq_lens, const int32_t* group_start,
+                              const int32_t* prefix_lens, int groups, int batch, int num_pages,
+                              float* out, void* stream);
 
 /* sync != 0: wait for the device, then return and clear the device error
    word (VATTN_DEV_* bits). sync == 0: return the host status of the last

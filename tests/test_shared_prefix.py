@@ -1,0 +1,293 @@
+"""vattn_shared_dense_decode against 64-bit attention over every sequence's own pages."""
+import math
+
+import pytest
+import torch
+
+from tests.serving import dense64, frequencies, rotate64, shared_batch
+from tests.test_append import _fake
+from verified_sparse_attention_b200 import _abi
+from verified_sparse_attention_b200.decoder import SparseDecoder
+from verified_sparse_attention_b200.rotary import Rotary
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ------------------------------------------------------------ refusals of the wrapper (CPU)
+def _args(**kw):
+    bf, i32 = torch.bfloat16, torch.int32
+    a = dict(q=torch.zeros(3, 8, 64, dtype=bf), k_cache=torch.zeros(5, 2, 16, 64, dtype=bf),
+             v_cache=torch.zeros(5, 2, 16, 64, dtype=bf), page_table=torch.zeros(3, 7, dtype=i32),
+             seq_lens=torch.ones(3, dtype=i32), num_pages=5, group_start=torch.tensor([0, 3], dtype=i32),
+             prefix_lens=torch.zeros(1, dtype=i32))
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=torch.zeros(3, 8, 64)), dict(q=torch.zeros(2, 8, 64, dtype=torch.bfloat16)),
+    dict(q=torch.zeros(8, 3, 64, dtype=torch.bfloat16).transpose(0, 1)),
+    dict(group_start=torch.tensor([0, 1, 3], dtype=torch.int32)), dict(group_start=torch.tensor([0, 3])),
+    dict(prefix_lens=torch.zeros(1)), dict(out=torch.zeros(3, 8, 64, dtype=torch.bfloat16)),
+    dict(out=torch.zeros(3, 8, 32)), dict(num_pages=6), dict(k_cache=torch.zeros(5, 2, 16, 64))])
+def test_shared_wrapper_refusals(bad):
+    with pytest.raises(ValueError):
+        _fake().shared_dense(**_args(**bad))
+
+
+def test_shared_needs_a_context():
+    with pytest.raises(_abi.VattnError):
+        _fake().shared_dense(**_args())
+
+
+# ------------------------------------------------------------ on the GPU
+def _tol(x, d):
+    """|out - exact| for one output, over max |v|.
+
+    A score is a sum of d exact products in fp32: d 2^-24 sum |q k| / sqrt(d) at most, sum |q k| under
+    3 d for these normal inputs; its scaling and the difference to the maximum add 2^-23 of |s| <= 16. The
+    weight exp2 adds 2^-21, and 2^-17 where it is split into two bf16 terms; the sums of weights and products
+    at most 2^-16 in all. Numerator and denominator: twice that."""
+    score = d * 2**-24 * 3 * d / math.sqrt(d) + 2**-19
+    return 2 * (score + 2**-21 + 2**-17 + 2**-16) * float(torch.nan_to_num(x["v_cache"].float()).abs().max())
+
+
+def _decoder(x, dtype, ps, **kw):
+    B, Hq, d = x["q"].shape
+    return SparseDecoder(num_q_heads=Hq, num_kv_heads=x["k_cache"].shape[1], head_dim=d, dtype=DT[dtype], page_size=ps,
+                         max_batch=kw.pop("max_batch", B), max_ctx=x["max_ctx"], **kw)
+
+
+def _cuda(x):
+    return {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+
+
+def _call(dec, x, **kw):
+    return dec.shared_dense(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"], x["num_pages"],
+                            x["group_start"], x["prefix_lens"], **kw)
+
+
+def _run(sizes, prefixes, own, *, dtype="bf16", d=128, Hq=8, Hkv=2, ps=16, seed=0, kv_location="device"):
+    x = shared_batch(sizes, prefixes, own, Hq=Hq, Hkv=Hkv, d=d, ps=ps, dtype=DT[dtype], seed=seed)
+    dec = _decoder(x, dtype, ps, kv_location=kv_location)
+    y = _cuda(x)
+    if kv_location == "host":
+        y["k_cache"], y["v_cache"] = x["k_cache"].pin_memory(), x["v_cache"].pin_memory()
+    got = _call(dec, y, out=torch.full((len(x["q"]), Hq, d), float("nan"), device="cuda")).cpu().double()
+    assert dec.last_error() == 0
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    assert (got[x["seq_lens"] == 0] == 0).all()
+    err = float((got - ref).abs().max())
+    assert err <= _tol(x, d), err
+    dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2), (4, 1), (16, 2)])
+@pytest.mark.parametrize("prefix", [1, 15, 16, 127, 128, 129, 1000])
+def test_shared_one_group(dtype, d, Hq, Hkv, prefix):
+    _run([5], [prefix], [0, 1, 17, 70, 3], dtype=dtype, d=d, Hq=Hq, Hkv=Hkv)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ps", [16, 32, 48, 64, 128, 2048])
+def test_shared_groups_of_every_kind(dtype, ps):
+    # alone, two, many; no prefix; sequences short of the prefix, at its end, empty; a group all empty
+    sizes = [1, 2, 9, 3, 2, 1, 4]
+    prefixes = [300, 257, 700, 0, 50, 0, 513]
+    own = [5, 40, 0, 1, 2, 3, -699, 0, 31, -700, -100, 64, 10, 0, 200, -50, -50, 129, 8, -1, 20, 0]
+    _run(sizes, prefixes, own, dtype=dtype, ps=ps)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Hq,Hkv", [(33, 8, 2), (40, 8, 1), (64, 8, 2), (70, 8, 2), (129, 8, 1), (150, 2, 2)])
+def test_shared_many_rows(dtype, B, Hq, Hkv):
+    # rows that fill one tile of 128 or 256, or pass it
+    _run([B], [400], [(7 * b) % 50 for b in range(B)], dtype=dtype, Hq=Hq, Hkv=Hkv, d=64)
+
+
+@pytest.mark.gpu
+def test_shared_long_prefix():
+    _run([6, 10], [20001, 9000], [(31 * b) % 300 for b in range(16)], Hq=16, Hkv=4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_host_caches(dtype):
+    _run([3, 2], [200, 77], [1, 20, 0, 5, 40], dtype=dtype, kv_location="host")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_large_scores_and_rising_maxima(dtype):
+    # keys that grow along the prefix: every tile raises the maximum, far above the earlier ones
+    x = shared_batch([40], [900], [(3 * b) % 40 for b in range(40)], Hq=8, Hkv=2, d=64, ps=16, dtype=DT[dtype], seed=3,
+                     garbage=0.0)
+    pages = x["page_table"][0, :56].long()
+    x["q"] = x["q"].abs()
+    grow = torch.linspace(0.0, 4.0, 56)[:, None, None, None]
+    x["k_cache"][pages] = (x["k_cache"][pages].float().abs() * grow).to(DT[dtype])
+    y = _cuda(x)
+    dec = _decoder(x, dtype, 16)
+    got = _call(dec, y).cpu().double()
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    # scores up to ~ 4 * 64 * 0.64 / 8 = 20 with partial sums as large: 4 times the products of _tol's bound
+    assert float((got - ref).abs().max()) <= 4 * _tol(x, 64)
+    assert dec.last_error() == 0
+    dec.close()
+
+
+@pytest.mark.gpu
+def test_shared_reports_and_zeroes_what_is_out_of_range():
+    x = shared_batch([3, 4], [100, 60], [5, 9, 0, 1, 30, 2, 8], Hq=8, Hkv=2, d=64, ps=16, dtype=torch.bfloat16)
+    dec = _decoder(x, "bf16", 16)
+    ref = _call(dec, _cuda(x)).cpu()
+    assert dec.last_error() == 0
+
+    def call(zero, bit, **kw):
+        got = _call(dec, _cuda(dict(x, **kw))).cpu()
+        assert dec.last_error() == bit
+        rest = [b for b in range(7) if b not in zero]
+        assert not got[zero].any()
+        # other splits of the work sum in another order
+        assert not rest or float((got[rest] - ref[rest]).abs().max()) <= 2 * _tol(x, 64)
+
+    def changed(key, at, value):
+        t = x[key].clone()
+        t[at] = value
+        return {key: t}
+
+    BAD_LEN, BAD_PAGE, BAD_GROUP = _abi.VATTN_DEV_BAD_SEQLEN, _abi.VATTN_DEV_BAD_PAGE, _abi.VATTN_DEV_BAD_GROUP
+    call([0, 1, 2], BAD_PAGE, **changed("page_table", (0, 2), x["num_pages"]))  # a prefix page of group 0
+    call([4], BAD_PAGE, **changed("page_table", (4, 5), -1))                    # an own page of sequence 4
+    call([1], BAD_LEN, **changed("seq_lens", 1, x["max_ctx"] + 1))
+    call([1], BAD_LEN, **changed("seq_lens", 1, -1))
+    call([3, 4, 5, 6], BAD_GROUP, **changed("prefix_lens", 1, x["max_ctx"] + 1))
+    call([3, 4, 5, 6], BAD_GROUP, **changed("prefix_lens", 1, -1))
+    every = list(range(7))
+    call(every, BAD_GROUP, **changed("group_start", 0, 1))
+    call(every, BAD_GROUP, **changed("group_start", 1, 9))
+    call(every, BAD_GROUP, **changed("group_start", 2, 6))
+    dec.close()
+
+
+@pytest.mark.gpu
+def test_shared_refusals_before_any_launch():
+    x = shared_batch([2], [20], [1, 2], Hq=8, Hkv=2, d=64, ps=16, dtype=torch.bfloat16)
+    dec = _decoder(x, "bf16", 16)
+    y = _cuda(x)
+    out = torch.full((2, 8, 64), 5.0, device="cuda")
+
+    def rc(**kw):
+        a = dict(q=y["q"], k_cache=y["k_cache"], v_cache=y["v_cache"], page_table=y["page_table"],
+                 seq_lens=y["seq_lens"], group_start=y["group_start"], prefix_lens=y["prefix_lens"], groups=1, batch=2,
+                 num_pages=x["num_pages"], out=out)
+        a.update(kw)
+        return _abi.vattn_shared_dense_decode(dec.ctx, *a.values(), check=False)
+
+    for bad in (dict(q=None), dict(k_cache=None), dict(page_table=None), dict(group_start=None),
+                dict(prefix_lens=None), dict(out=None), dict(groups=0), dict(groups=3), dict(batch=-1), dict(batch=3),
+                dict(num_pages=0), dict(q=y["q"].data_ptr() + 2), dict(k_cache=y["k_cache"].data_ptr() + 8)):
+        assert rc(**bad) == _abi.VATTN_EINVAL, bad
+    assert rc(batch=0, groups=0, q=None) == _abi.VATTN_OK
+    assert (out == 5).all()
+    dec.close()
+
+
+@pytest.mark.gpu
+def test_shared_captured_on_another_stream_with_a_padded_batch():
+    x = shared_batch([6, 5], [300, 130], [(5 * b) % 20 for b in range(11)], Hq=8, Hkv=2, d=64, ps=16,
+                     dtype=torch.bfloat16)
+    dec = _decoder(x, "bf16", 16)
+    y = _cuda(x)
+    out = torch.zeros(11, 8, 64, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=s):
+        _call(dec, y, out=out)
+    # a step later: other lengths, two slots empty, the second group larger
+    lens = x["seq_lens"].clone()
+    lens[3] = 0
+    lens[10] = 0
+    y["seq_lens"].copy_(lens)
+    graph.replay()
+    got = out.cpu().double()
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], lens)
+    assert float((got - ref).abs().max()) <= _tol(x, 64)
+    assert dec.last_error() == 0
+    dec.close()
+
+
+@pytest.mark.gpu
+def test_shared_equals_dense_and_is_reproducible():
+    x = shared_batch([20], [2000], [(11 * b) % 90 for b in range(20)], Hq=16, Hkv=4, d=128, ps=16, dtype=torch.bfloat16,
+                     garbage=0.0)
+    dec = _decoder(x, "bf16", 16)
+    y = _cuda(x)
+    a, b = _call(dec, y), _call(dec, y)
+    assert torch.equal(a, b)
+    dense = dec.dense(y["q"], y["k_cache"], y["v_cache"], y["page_table"], y["seq_lens"], y["num_pages"])
+    assert float((a - dense).abs().max()) <= 2 * _tol(x, 128)
+    dec.close()
+
+
+# ------------------------------------------------------------ as they are used together
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_serving_steps(dtype):
+    """Append a shared prompt once, then decode steps: append with rotation, shared decode, sparse decode."""
+    dt, d, Hq, Hkv, ps, B, prompt, steps = DT[dtype], 64, 8, 2, 16, 5, 75, 4
+    g = torch.Generator().manual_seed(11)
+    rotary = Rotary(head_dim=d, rot_dim=32, scaling="linear", factor=2.0)
+    freq = frequencies(32, scaling="linear", factor=2.0)
+    max_ctx = prompt + steps
+    pps = -(-max_ctx // ps)
+    whole = prompt // ps
+    # every sequence lists the prompt's whole pages, and pages of its own behind them
+    table = torch.zeros(B, pps, dtype=torch.int32)
+    table[:, :whole] = torch.arange(whole)
+    table[:, whole:] = whole + torch.arange(B * (pps - whole)).view(B, -1)
+    pages = whole + B * (pps - whole)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k_cache = torch.full((pages, Hkv, ps, d), float("nan"), dtype=dt, device="cuda")
+    v_cache = torch.full((pages, Hkv, ps, d), float("nan"), dtype=dt, device="cuda")
+    dec = SparseDecoder(num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d, dtype=dt, page_size=ps, max_batch=B,
+                        max_ctx=max_ctx)
+    K = torch.randn(prompt, Hkv, d, generator=g).to(dt)
+    V = torch.randn(prompt, Hkv, d, generator=g).to(dt)
+    tab = table.cuda()
+    # the prompt once into sequence 0's pages; the page it ends in copied to the others'
+    dec.append(K.cuda(), V.cuda(), k_cache, v_cache, tab[:1], torch.tensor([prompt], **i32), pages,
+               cu_tokens=torch.tensor([0, prompt], **i32), rotary=rotary)
+    for c in (k_cache, v_cache):
+        c[tab[1:, whole].long()] = c[tab[0, whole].long()].clone()
+    hist_k = [rotate64(K, torch.arange(prompt), 32, "half", freq).to(dt)] * B
+    hist_v = [V] * B
+    seq_lens = torch.full((B,), prompt, **i32)
+    group_start, prefix = torch.tensor([0, B], **i32), torch.tensor([prompt], **i32)
+    for step in range(steps):
+        seq_lens += 1
+        q, k, v = (torch.randn(B, h, d, generator=g).to(dt) for h in (Hq, Hkv, Hkv))
+        qr = dec.append(k.cuda(), v.cuda(), k_cache, v_cache, tab, seq_lens, pages, rotary=rotary, q=q.cuda())
+        shared = dec.shared_dense(qr, k_cache, v_cache, tab, seq_lens, pages, group_start, prefix)
+        params = SparseDecoder.make_params(sinks=4, window=max_ctx, eps=0.1, delta=0.1, seed=0, num_pages=pages)
+        sparse = dec.decode(qr, k_cache, v_cache, tab, seq_lens, params)["out"]   # the window covers everything
+        assert dec.last_error() == 0
+        pos = torch.full((B,), prompt + step)
+        kr, q64 = rotate64(k, pos, 32, "half", freq), rotate64(q, pos, 32, "half", freq)
+        hist_k = [torch.cat([h, kr[b:b + 1].to(dt)]) for b, h in enumerate(hist_k)]
+        hist_v = [torch.cat([h, v[b:b + 1]]) for b, h in enumerate(hist_v)]
+        for b in range(B):
+            s = q64[b].to(dt).double().view(Hkv, -1, d) @ hist_k[b].double().permute(1, 2, 0) / math.sqrt(d)
+            ref = (torch.softmax(s, -1) @ hist_v[b].double().transpose(0, 1)).reshape(Hq, d)
+            # the rotated rows may round to the neighbouring value where fp32 and 64 bits straddle a tie:
+            # half an ulp (bf16 2^-9 of a product at most, 16 of them at random signs) of a score
+            tol = (2**-6 if dtype == "bf16" else 2**-14) * float(V.float().abs().max())
+            assert float((shared[b].cpu().double() - ref).abs().max()) <= tol
+            assert float((sparse[b].cpu().double() - ref).abs().max()) <= tol
+    dec.close()

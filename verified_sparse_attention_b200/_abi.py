@@ -16,13 +16,16 @@ VATTN_EXACT, VATTN_SPARQ, VATTN_LOKI = 0, 1, 2
 VATTN_KV_DEVICE, VATTN_KV_HOST = 0, 1
 VATTN_GUARANTEE_DENOMINATOR, VATTN_GUARANTEE_OUTPUT = 0, 1
 VATTN_OK, VATTN_EINVAL, VATTN_ENOMEM, VATTN_ECUDA, VATTN_ESCRATCH = 0, -1, -2, -3, -4
-VATTN_DEV_BAD_SEQLEN, VATTN_DEV_BAD_PAGE, VATTN_DEV_TIMEOUT = 1, 2, 4
+VATTN_DEV_BAD_SEQLEN, VATTN_DEV_BAD_PAGE, VATTN_DEV_TIMEOUT, VATTN_DEV_BAD_GROUP = 1, 2, 4, 8
+VATTN_ROPE_HALF, VATTN_ROPE_INTERLEAVED = 0, 1
+VATTN_ROPE_NONE, VATTN_ROPE_LINEAR, VATTN_ROPE_BASE, VATTN_ROPE_BANDS, VATTN_ROPE_YARN = 0, 1, 2, 3, 4
 
 # every symbol include/vattn.h declares
 EXPORTS = ("vattn_create", "vattn_decode", "vattn_dense_decode", "vattn_dense_decode_static",
            "vattn_last_error", "vattn_check_bounded_wait",
            "vattn_workspace_bytes", "vattn_set_timing", "vattn_score_pass_ms",
-           "vattn_last_launch_count", "vattn_strerror", "vattn_destroy")
+           "vattn_last_launch_count", "vattn_strerror", "vattn_destroy",
+           "vattn_rope_init", "vattn_rotate", "vattn_append", "vattn_shared_dense_decode")
 
 
 class vattn_config(C.Structure):
@@ -41,6 +44,26 @@ class vattn_params(C.Structure):
                 ("k_t_cache", C.c_void_p), ("k_proj_cache", C.c_void_p), ("proj_basis", C.c_void_p),
                 ("guarantee", C.c_int), ("topp_num", C.c_int), ("topp_den", C.c_int),
                 ("batch_offset", C.c_int), ("head_offset", C.c_int)]
+
+
+class vattn_rope_config(C.Structure):
+    _fields_ = [("head_dim", C.c_int), ("rot_dim", C.c_int), ("layout", C.c_int), ("scaling", C.c_int),
+                ("base", C.c_double), ("factor", C.c_double), ("original_ctx", C.c_double),
+                ("low", C.c_double), ("high", C.c_double), ("slow", C.c_double), ("fast", C.c_double),
+                ("amplitude", C.c_double)]
+
+
+class vattn_rope(C.Structure):
+    _fields_ = [("head_dim", C.c_int), ("rot_dim", C.c_int), ("layout", C.c_int),
+                ("amplitude", C.c_float), ("turns", C.c_uint64 * 64)]
+
+
+class vattn_append_params(C.Structure):
+    _fields_ = [("rope", C.POINTER(vattn_rope)), ("tokens", C.c_int), ("num_pages", C.c_int),
+                ("cu_tokens", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q", C.c_void_p),
+                ("k_stride", C.c_longlong), ("v_stride", C.c_longlong), ("q_stride", C.c_longlong),
+                ("q_out", C.c_void_p), ("k_cache", C.c_void_p), ("v_cache", C.c_void_p),
+                ("k_t_cache", C.c_void_p), ("k_proj_cache", C.c_void_p), ("proj_basis", C.c_void_p)]
 
 
 class VattnError(RuntimeError):
@@ -81,6 +104,15 @@ def lib():
         L.vattn_last_launch_count.restype = I
         L.vattn_strerror.argtypes = [I]
         L.vattn_strerror.restype = C.c_char_p
+        L.vattn_rope_init.argtypes = [C.POINTER(vattn_rope), C.POINTER(vattn_rope_config)]
+        L.vattn_rope_init.restype = I
+        X = C.c_longlong
+        L.vattn_rotate.argtypes = [C.POINTER(vattn_rope), P, P, P, I, I, I, X, X, X, X, I, P]
+        L.vattn_rotate.restype = I
+        L.vattn_append.argtypes = [P, C.POINTER(vattn_append_params), P, P, I, P]
+        L.vattn_append.restype = I
+        L.vattn_shared_dense_decode.argtypes = [P, P, P, P, P, P, P, P, I, I, I, P, P]
+        L.vattn_shared_dense_decode.restype = I
         L.vattn_destroy.argtypes = [P]
         L.vattn_destroy.restype = None
         _LIB = L
@@ -146,6 +178,39 @@ def vattn_dense_decode_static(config, q, k_cache, v_cache, page_table, seq_lens,
                                          _ptr(page_table), _ptr(seq_lens), int(batch),
                                          int(num_pages), _ptr(out), _stream_ptr(stream))
     return _check(rc, "vattn_dense_decode_static") if check else rc
+
+
+def vattn_rope_init(config):
+    """A rotation plan (vattn_rope) from a vattn_rope_config (or a dict of its fields)."""
+    if isinstance(config, dict):
+        config = vattn_rope_config(**config)
+    rope = vattn_rope()
+    _check(lib().vattn_rope_init(C.byref(rope), C.byref(config)), "vattn_rope_init")
+    return rope
+
+
+def vattn_rotate(rope, x, out, positions, tokens, heads, dtype, x_strides, out_strides, transpose=False,
+                 stream=None, check=True):
+    """Rotate x into out; the strides are (token, head) in elements."""
+    rc = lib().vattn_rotate(rope, _ptr(x), _ptr(out), _ptr(positions), tokens, heads, dtype, *x_strides,
+                            *out_strides, 1 if transpose else 0, _stream_ptr(stream))
+    return _check(rc, "vattn_rotate") if check else rc
+
+
+def vattn_append(ctx, params, page_table, seq_lens, batch, stream=None, check=True):
+    """Append new tokens to the caches (see include/vattn.h); returns the C return code."""
+    if isinstance(params, dict):
+        params = vattn_append_params(**params)
+    rc = lib().vattn_append(ctx, params, _ptr(page_table), _ptr(seq_lens), batch, _stream_ptr(stream))
+    return _check(rc, "vattn_append") if check else rc
+
+
+def vattn_shared_dense_decode(ctx, q, k_cache, v_cache, page_table, seq_lens, group_start, prefix_lens, groups,
+                              batch, num_pages, out, stream=None, check=True):
+    rc = lib().vattn_shared_dense_decode(ctx, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
+                                         _ptr(seq_lens), _ptr(group_start), _ptr(prefix_lens), int(groups),
+                                         int(batch), int(num_pages), _ptr(out), _stream_ptr(stream))
+    return _check(rc, "vattn_shared_dense_decode") if check else rc
 
 
 def vattn_last_error(ctx, sync=True):

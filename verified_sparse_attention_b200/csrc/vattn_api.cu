@@ -1,63 +1,22 @@
 // Host side of the C ABI declared in include/vattn.h: argument checks,
 // workspace, template dispatch and the launch sequence of one decode step.
-#include <cuda_runtime.h>
-#include <math.h>
 #include <stdlib.h>
-#include <string.h>
 
 #include <algorithm>
 #include <type_traits>
-#include <vector>
 
-#include "vattn.h"
+#include "vattn_ctx.h"
 #include "vattn_kernels.cuh"
 
+using vattn::align256;
+using vattn::aligned16;
+using vattn::cache_ptrs;
 using vattn::DevParams;
+using vattn::encode_row_maps;
+using vattn::fill_common;
+using vattn::finish;
+using vattn::launch;
 using vattn::UnitInfo;
-
-struct vattn_ctx {
-  vattn_config cfg;
-  int device = 0;
-  int num_sms = 0;
-  int G = 1;
-  int units_max = 0;
-  int score_grid = 0;
-  bool score_tma = false;   // contiguous cache: the bulk-copy score pass
-  size_t score_smem = 0;
-  int gather_grid = 0;     // CTAs of each gather launch
-  int CD = 0, CS = 0;      // record producers (warps) of the det/dense and sample gathers
-  size_t gather_smem = 0;   // gathers (all modes)
-  int gather_threads = 0;
-  int draw_splits = 1;
-  size_t ws_bytes = 0;
-  void* ws = nullptr;
-  // carved workspace
-  UnitInfo* info = nullptr;
-  float* qbar = nullptr;
-  float* qsel = nullptr;
-  int* dims = nullptr;
-  unsigned* ordk = nullptr;
-  unsigned* hist = nullptr;
-  float* pscore = nullptr;
-  int* num_need = nullptr;
-  long long* prefix = nullptr;
-  unsigned* gcnt = nullptr;
-  long long* pre_det = nullptr;
-  long long* pre_samp = nullptr;
-  float* rec_det = nullptr;
-  float* rec_samp = nullptr;
-  unsigned* err = nullptr;
-  // state
-  int last_status = VATTN_OK;
-  int last_launches = 0;
-  double cached_delta = -1.0;
-  double cached_z = 0.0;
-  // timing of the score pass
-  int timing = 0;            // period (0: off)
-  long long timing_calls = 0;
-  std::vector<cudaEvent_t> ev_start, ev_stop;
-  size_t ev_used = 0;
-};
 
 namespace {
 
@@ -74,59 +33,6 @@ double normal_upper_quantile(double delta) {
       hi = mid;
   }
   return 0.5 * (lo + hi);
-}
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// The driver's tensor-map encoder, reached through the runtime (the library
-// does not link the driver library itself).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static const EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return static_cast<EncodeTiledFn>(nullptr);
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
-
-// Row maps of the K and V caches for the gathers: a 2-D [rows][d] view with
-// rows = num_pages * Hkv * page_size, one-row boxes of all d columns.
-int encode_row_maps(const vattn_config& c, const void* k, const void* v, int num_pages, DevParams* P) {
-  const unsigned long long rows =
-      static_cast<unsigned long long>(num_pages) * c.num_kv_heads * static_cast<unsigned long long>(c.page_size);
-  if (rows > 0x7FFFFFFFull) return VATTN_EINVAL;  // row coordinates are 32-bit
-  const EncodeTiledFn fn = encode_tiled();
-  if (!fn) return VATTN_ECUDA;
-  const cuuint64_t esz = c.dtype == VATTN_BF16 ? 2 : 4;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.head_dim), rows};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.head_dim) * esz};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(c.head_dim), 1u};
-  const cuuint32_t estr[2] = {1u, 1u};
-  const CUtensorMapDataType dt =
-      c.dtype == VATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-  for (int i = 0; i < 2; i++) {
-    const CUresult r = fn(i ? &P->tmv : &P->tmk, dt, 2, const_cast<void*>(i ? v : k), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return VATTN_ECUDA;
-  }
-  if (c.dtype == VATTN_BF16) {  // the tensor-core gathers' swizzled half-row boxes
-    const cuuint32_t hbox[2] = {64u, 1u};
-    for (int i = 0; i < 2; i++) {
-      const CUresult r = fn(i ? &P->tmv_sw : &P->tmk_sw, dt, 2, const_cast<void*>(i ? v : k), dims, strides, hbox,
-                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-      if (r != CUDA_SUCCESS) return VATTN_ECUDA;
-    }
-  }
-  return VATTN_OK;
 }
 
 // ---------------------------------------------------------------- dispatch
@@ -231,99 +137,11 @@ int check_config(const vattn_config* c) {
   return VATTN_OK;
 }
 
-// Device address of a cache in page-locked host memory (nullptr if `p` is not
-// such memory).
-const void* host_cache_device_ptr(const void* p) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();
-    return nullptr;
-  }
-  if (a.type != cudaMemoryTypeHost || a.devicePointer == nullptr) return nullptr;
-  return static_cast<const char*>(a.devicePointer) +
-         (static_cast<const char*>(p) - static_cast<const char*>(a.hostPointer ? a.hostPointer : p));
-}
-
-// The caches as the kernels address them (host-resident caches mapped to
-// their device addresses); VATTN_EINVAL if a host-resident cache is not
-// page-locked.
-int cache_ptrs(const vattn_config& c, const void** k, const void** v) {
-  if (c.kv_location != VATTN_KV_HOST) return VATTN_OK;
-  const void* dk = host_cache_device_ptr(*k);
-  const void* dv = host_cache_device_ptr(*v);
-  if (!dk || !dv) return VATTN_EINVAL;
-  *k = dk;
-  *v = dv;
-  return VATTN_OK;
-}
-
-void fill_common(const vattn_ctx* ctx, DevParams* P, int batch) {
-  memset(P, 0, sizeof(*P));
-  const vattn_config& c = ctx->cfg;
-  P->Hq = c.num_q_heads;
-  P->Hkv = c.num_kv_heads;
-  P->G = ctx->G;
-  P->D = c.head_dim;
-  P->pps = (c.max_ctx + c.page_size - 1) / c.page_size;
-  P->ps = c.page_size;
-  P->ps_magic = ~0ull / static_cast<unsigned long long>(c.page_size) + 1ull;
-  P->max_ctx = c.max_ctx;
-  P->batch = batch;
-  P->units = batch * c.num_kv_heads;
-  P->proxy = c.proxy;
-  P->rank = c.proxy_rank;
-  P->kv_host = c.kv_location == VATTN_KV_HOST;
-  P->scale = static_cast<float>(1.0 / sqrt(static_cast<double>(c.head_dim)));
-  P->info = ctx->info;
-  P->qbar = ctx->qbar;
-  P->qsel = ctx->qsel;
-  P->dims = ctx->dims;
-  P->ordk = ctx->ordk;
-  P->hist = ctx->hist;
-  P->pscore = ctx->pscore;
-  P->num_need = ctx->num_need;
-  P->prefix = ctx->prefix;
-  P->gcnt = ctx->gcnt;
-  P->pre_det = ctx->pre_det;
-  P->pre_samp = ctx->pre_samp;
-  P->rec_det = ctx->rec_det;
-  P->rec_samp = ctx->rec_samp;
-  P->CD = ctx->CD;
-  P->CS = ctx->CS;
-  P->err = ctx->err;
-}
-
-// Launch with programmatic dependent launch: the kernel may be scheduled while
-// its predecessor on the stream drains; it waits (griddepcontrol.wait) before
-// reading the predecessor's results.
-void launch(void (*kern)(DevParams), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const DevParams& P,
-            int* count) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kern, P);
-  (*count)++;
-}
-
 // Threads of a combine CTA (one per unit and head): sixteen warps while the
 // CTAs fit one wave at two per SM, else eight.
 int comb_threads(const vattn_ctx* ctx, int units) {
   const long long ctas = static_cast<long long>(units) * ctx->G;
   return (ctas <= 2LL * ctx->num_sms ? vattn::kCombWarps : vattn::kCombWarps / 2) * 32;
-}
-
-int finish(vattn_ctx* ctx, int launches) {
-  ctx->last_launches = launches;
-  const cudaError_t e = cudaGetLastError();
-  ctx->last_status = e == cudaSuccess ? VATTN_OK : VATTN_ECUDA;
-  return ctx->last_status;
 }
 
 }  // namespace
@@ -412,8 +230,9 @@ int vattn_create(vattn_ctx** out, const vattn_config* cfg) {
   const size_t sz_rdet = align256((ctx->CD + 2 * U) * REC * sizeof(float));
   const size_t sz_rsmp = align256((ctx->CS + 2 * U) * REC * sizeof(float));
   const size_t sz_err = 256;
+  const size_t sz_shared = vattn::shared_workspace(ctx, nullptr);
   ctx->ws_bytes = sz_info + 3 * sz_vec + sz_ordk + sz_hist + sz_ps + sz_nneed + sz_pre + sz_gcnt +
-                  2 * sz_spre + sz_rdet + sz_rsmp + sz_err;
+                  2 * sz_spre + sz_rdet + sz_rsmp + sz_err + sz_shared;
   if (cudaMalloc(&ctx->ws, ctx->ws_bytes) != cudaSuccess) {
     cudaGetLastError();
     delete ctx;
@@ -434,7 +253,8 @@ int vattn_create(vattn_ctx** out, const vattn_config* cfg) {
   ctx->pre_samp = reinterpret_cast<long long*>(p); p += sz_spre;
   ctx->rec_det = reinterpret_cast<float*>(p); p += sz_rdet;
   ctx->rec_samp = reinterpret_cast<float*>(p); p += sz_rsmp;
-  ctx->err = reinterpret_cast<unsigned*>(p);
+  ctx->err = reinterpret_cast<unsigned*>(p); p += sz_err;
+  vattn::shared_workspace(ctx, p);
   if (cudaMemset(ctx->ws, 0, ctx->ws_bytes) != cudaSuccess) {
     cudaFree(ctx->ws);
     delete ctx;

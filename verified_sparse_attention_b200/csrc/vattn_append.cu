@@ -1,0 +1,609 @@
+// Rotary positions and appending to the cache (vattn_rope_init, vattn_rotate,
+// vattn_append).
+//
+// Both kernels stream rows of d components: every thread owns one chunk pair
+// (2 x 16 bytes) of a token's heads, computes the E cosines and sines of its
+// pairs once and then walks over the token's heads, so that no table, shared
+// memory or barrier stands between the loads and the stores. Bound by HBM for
+// prompts and by the launch for single tokens.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "vattn_ctx.h"
+
+namespace {
+
+using vattn::aligned16;
+using vattn::Elem;
+
+constexpr int kThreads = 256;
+constexpr int kMaxTok = 64;   // tokens of a block at most
+constexpr int kMaxTokens = 1 << 30, kMaxHeads = 1 << 16;  // of a call
+constexpr int kRank = 32;     // components of a projected key (Loki)
+constexpr unsigned kDevBadSeqlen = VATTN_DEV_BAD_SEQLEN, kDevBadPage = VATTN_DEV_BAD_PAGE;
+
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// cos and sin of pair i at position pos: the position times the pair's turns
+// wraps modulo one turn in 64-bit integers; the nearest quarter turn is taken
+// out of the upper 32 bits exactly, and the rest, within an eighth of a turn
+// (2^-32 of a turn exact, 2^-25 relative as fp32), goes through sincospif.
+__device__ __forceinline__ void pair_turn(const vattn_rope& R, int i, int pos, bool transpose, float& c, float& s) {
+  const unsigned t =
+      static_cast<unsigned>((R.turns[i] * static_cast<unsigned long long>(static_cast<long long>(pos))) >> 32);
+  const unsigned quarter = (t + 0x20000000u) >> 30;
+  const int rest = static_cast<int>(t - (quarter << 30));
+  float sr, cr;
+  sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &sr, &cr);  // 2^-31: half turns
+  s = (quarter & 1u) ? cr : sr;
+  c = (quarter & 1u) ? sr : cr;
+  if (quarter & 2u) s = -s;
+  if ((quarter + 1u) & 2u) c = -c;
+  if (transpose) s = -s;
+  c *= R.amplitude;
+  s *= R.amplitude;
+}
+
+// E elements as one load and store (16 bytes, or a single element).
+template <typename T, int E>
+struct Chunk {
+  uint4 raw;
+  __device__ __forceinline__ void load(const T* p) { raw = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = raw; }
+  __device__ __forceinline__ void get(float (&x)[E]) const { Elem<T>::unpack(raw, x); }
+  __device__ __forceinline__ void set(const float (&x)[E]) {
+    if constexpr (sizeof(T) == 4) {
+      raw = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    } else {
+      unsigned w[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const unsigned*>(&v);
+      }
+      raw = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+};
+template <typename T>
+struct Chunk<T, 1> {
+  T raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = raw; }
+  __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = static_cast<float>(raw); }
+  __device__ __forceinline__ void set(const float (&x)[1]) { raw = static_cast<T>(x[0]); }
+};
+
+// A thread's two chunks of a row and the turns of its E pairs. Chunk pair p of
+// the D / 2E of a row: in the half layout chunks p and p + rot / 2E while these
+// rotate, else two neighbours behind rot_dim; in the interleaved layout chunks
+// 2p and 2p + 1. E divides rot_dim / 2.
+template <typename T, int D, int E>
+struct Pair {
+  int a, b;      // first elements of the two chunks
+  bool turned, half;
+  float c[E], s[E];
+  __device__ __forceinline__ void place(const vattn_rope& R, int p) {
+    half = R.layout == VATTN_ROPE_HALF;
+    turned = p * E < R.rot_dim / 2;
+    a = half && turned ? p * E : 2 * p * E;
+    b = half && turned ? R.rot_dim / 2 + p * E : a + E;
+  }
+  __device__ __forceinline__ void turn(const vattn_rope& R, int p, int pos, bool transpose) {
+    if (!turned) return;
+#pragma unroll
+    for (int e = 0; e < E; e++) pair_turn(R, p * E + e, pos, transpose, c[e], s[e]);
+  }
+  // one rounding per product and sum, the same in every variant
+  __device__ static __forceinline__ void turn_pair(float& u, float& v, float c, float s) {
+    const float w = __fmaf_rn(u, c, -__fmul_rn(v, s));
+    v = __fmaf_rn(v, c, __fmul_rn(u, s));
+    u = w;
+  }
+  __device__ __forceinline__ void apply(Chunk<T, E>& ca, Chunk<T, E>& cb) const {
+    float x[E], y[E];
+    ca.get(x);
+    cb.get(y);
+    if (half || E == 1) {
+#pragma unroll
+      for (int e = 0; e < E; e++) turn_pair(x[e], y[e], c[e], s[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E / 2; e++) {
+        turn_pair(x[2 * e], x[2 * e + 1], c[e], s[e]);
+        turn_pair(y[2 * e], y[2 * e + 1], c[E / 2 + e], s[E / 2 + e]);
+      }
+    }
+    ca.set(x);
+    cb.set(y);
+  }
+};
+
+// ---------------------------------------------------------------- rotate
+struct RotateArgs {
+  vattn_rope rope;
+  const void* x;
+  void* out;
+  const int* positions;
+  int tokens, heads, transpose;
+  int lanes, tok_block;  // threads that share a token's heads (per chunk pair); tokens of a block
+  long long xt, xh, ot, oh;
+};
+
+constexpr int kUnroll = 4;  // rows whose loads a thread issues together
+
+template <typename T, int D, int E>
+__global__ void __launch_bounds__(kThreads) k_rotate(const __grid_constant__ RotateArgs A) {
+  constexpr int NP = D / (2 * E);
+  const int p = threadIdx.x % NP, rest = threadIdx.x / NP;
+  const int hl = kThreads / NP / A.tok_block;  // head lanes of a block
+  const int t = blockIdx.x * A.tok_block + rest / hl;
+  const int r0 = blockIdx.y * hl + rest % hl;
+  dependency_wait();
+  if (t >= A.tokens || r0 >= A.heads) return;
+  Pair<T, D, E> P;
+  P.place(A.rope, p);
+  P.turn(A.rope, p, A.positions[t], A.transpose != 0);
+  const T* x = static_cast<const T*>(A.x) + t * A.xt;
+  T* out = static_cast<T*>(A.out) + t * A.ot;
+  for (int r = r0; r < A.heads; r += kUnroll * A.lanes) {
+    Chunk<T, E> ca[kUnroll], cb[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; k++) {
+      const int h = r + k * A.lanes;
+      if (h >= A.heads) break;
+      ca[k].load(x + h * A.xh + P.a);
+      cb[k].load(x + h * A.xh + P.b);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; k++) {
+      const int h = r + k * A.lanes;
+      if (h >= A.heads) break;
+      if (P.turned) P.apply(ca[k], cb[k]);
+      ca[k].store(out + h * A.oh + P.a);
+      cb[k].store(out + h * A.oh + P.b);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- append
+struct AppendArgs {
+  vattn_rope rope;   // rot_dim = 0: no rotation
+  const void *k, *v, *q;
+  long long ks, vs, qs;
+  void *q_out, *k_cache, *v_cache, *k_t, *k_proj;
+  const float* basis;
+  const int *page_table, *seq_lens, *cu;
+  unsigned* err;
+  int tokens, batch, Hq, Hkv, ps, pps, max_ctx, num_pages;
+  int key_blocks;        // proxies: blocks that take one head of a tile of tokens each
+  int lanes, tok_block;  // as in RotateArgs
+  int row_y;             // blocks that share a token's rows
+};
+
+// Position and cache row (page * Hkv * ps + slot; -1: nothing to write) of
+// tokens [t0, t0 + n) into shared memory, by the whole block. Every sequence
+// marks its own tokens of the range, in one round of loads.
+__device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_pos, long long* s_row) {
+  if (A.cu != nullptr) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) s_seq[i] = -1;
+    __syncthreads();
+    for (int b = threadIdx.x; b < A.batch; b += blockDim.x) {
+      const int lo = A.cu[b], hi = A.cu[b + 1];
+      if (lo < 0 || hi < lo || hi > A.tokens) {
+        if (t0 == 0) atomicOr(A.err, kDevBadSeqlen);
+        continue;
+      }
+      const int e = min(hi, t0 + n);
+      if (e <= max(lo, t0)) continue;
+      const int len = A.seq_lens[b], before = len - (hi - lo);
+      if (before < 0 || len > A.max_ctx) {
+        atomicOr(A.err, kDevBadSeqlen);
+        continue;
+      }
+      for (int t = max(lo, t0); t < e; t++) {
+        s_seq[t - t0] = b;
+        s_pos[t - t0] = before + (t - lo);
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    long long row = -1;
+    int b, pos;
+    if (A.cu != nullptr) {
+      b = s_seq[i];
+      pos = b < 0 ? -1 : s_pos[i];
+    } else {
+      b = t0 + i;
+      pos = A.seq_lens[b] - 1;
+      if (pos < -1 || pos >= A.max_ctx) {
+        atomicOr(A.err, kDevBadSeqlen);
+        pos = -1;
+      }
+      s_pos[i] = pos;
+    }
+    if (pos >= 0) {
+      const int slot = pos / A.ps;
+      const int page = A.page_table[static_cast<size_t>(b) * A.pps + slot];
+      if (page < 0 || page >= A.num_pages)
+        atomicOr(A.err, kDevBadPage);
+      else
+        row = static_cast<long long>(page) * A.Hkv * A.ps + (pos - slot * A.ps);
+    }
+    s_row[i] = row;
+  }
+  __syncthreads();
+}
+
+// Tokens of a key tile: its stored keys stay in shared memory for the
+// transposed or projected copy.
+template <typename T>
+constexpr int kKeyTile = sizeof(T) == 2 ? 64 : 32;
+
+template <typename T, int D, int E, int PROXY>
+__global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ AppendArgs A) {
+  constexpr int NP = D / (2 * E);
+  __shared__ int s_seq[kMaxTok], s_pos[kMaxTok];
+  __shared__ long long s_row[kMaxTok];
+  dependency_wait();
+  int blk = blockIdx.x;
+  if constexpr (PROXY != VATTN_EXACT) {
+    if (blk < A.key_blocks) {
+      constexpr int TT = kKeyTile<T>;
+      constexpr int PAD = 16 / sizeof(T) + 4 / sizeof(T);
+      __shared__ __align__(16) T s_key[TT][D + PAD];
+      const int h = blk % A.Hkv, t0 = blk / A.Hkv * TT;
+      const int n = min(TT, A.tokens - t0);
+      resolve(A, t0, n, s_seq, s_pos, s_row);
+      const int p = threadIdx.x % NP;
+      Pair<T, D, E> P;
+      P.place(A.rope, p);
+      for (int i = threadIdx.x / NP; i < n; i += kThreads / NP) {
+        if (s_row[i] < 0) continue;
+        P.turn(A.rope, p, s_pos[i], false);
+        const T* x = static_cast<const T*>(A.k) + (t0 + i) * A.ks + h * D;
+        Chunk<T, E> ca, cb;
+        ca.load(x + P.a);
+        cb.load(x + P.b);
+        if (P.turned) P.apply(ca, cb);
+        T* o = static_cast<T*>(A.k_cache) + static_cast<size_t>(s_row[i] + h * A.ps) * D;
+        ca.store(o + P.a);
+        cb.store(o + P.b);
+        const T* ra = reinterpret_cast<const T*>(&ca.raw);
+        const T* rb = reinterpret_cast<const T*>(&cb.raw);
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+          s_key[i][P.a + e] = ra[e];
+          s_key[i][P.b + e] = rb[e];
+        }
+      }
+      __syncthreads();
+      if constexpr (PROXY == VATTN_SPARQ) {
+        // neighbouring lanes hold neighbouring tokens, whose slots are neighbours too
+        const int i = threadIdx.x % TT;
+        if (i >= n || s_row[i] < 0) return;
+        // row = page * Hkv * ps + slot: the page's dim-major block starts at (page * Hkv + h) * D * ps
+        const long long head = s_row[i] / A.ps + h, slot = s_row[i] % A.ps;
+        T* o = static_cast<T*>(A.k_t) + static_cast<size_t>(head) * D * A.ps + slot;
+        for (int j = threadIdx.x / TT; j < D; j += kThreads / TT) o[static_cast<size_t>(j) * A.ps] = s_key[i][j];
+      } else {
+        __shared__ __align__(16) float s_basis[D][kRank];
+        const float* basis = A.basis + static_cast<size_t>(h) * D * kRank;
+        for (int i = threadIdx.x; i < D * kRank; i += kThreads) (&s_basis[0][0])[i] = basis[i];
+        __syncthreads();
+        for (int x = threadIdx.x; x < n * kRank; x += kThreads) {
+          const int i = x / kRank, r = x % kRank;
+          if (s_row[i] < 0) continue;
+          float acc = 0.0f;
+#pragma unroll 8
+          for (int j = 0; j < D; j++) acc = fmaf(static_cast<float>(s_key[i][j]), s_basis[j][r], acc);
+          static_cast<T*>(A.k_proj)[static_cast<size_t>(s_row[i] + h * A.ps) * kRank + r] = static_cast<T>(acc);
+        }
+      }
+      return;
+    }
+    blk -= A.key_blocks;
+  }
+  // the other rows of tok_block tokens: keys (no proxy), values, queries
+  const int hl = kThreads / NP / A.tok_block;
+  const int t0 = blk / A.row_y * A.tok_block;
+  const int n = min(A.tok_block, A.tokens - t0);
+  resolve(A, t0, n, s_seq, s_pos, s_row);
+  const int p = threadIdx.x % NP, rest = threadIdx.x / NP;
+  const int i = rest / hl;
+  if (i >= n || s_row[i] < 0) return;
+  const int nk = PROXY == VATTN_EXACT ? A.Hkv : 0;
+  const int rows = nk + A.Hkv + (A.q != nullptr ? A.Hq : 0);
+  const int r0 = blk % A.row_y * hl + rest % hl;
+  if (r0 >= rows) return;
+  Pair<T, D, E> P;
+  P.place(A.rope, p);
+  P.turn(A.rope, p, s_pos[i], false);
+  const long long t = t0 + i;
+  const long long row = s_row[i];
+  // rows in the order keys, queries, values
+  const int nq = rows - A.Hkv;
+  auto src = [&](int r) -> const T* {
+    if (r < nk) return static_cast<const T*>(A.k) + t * A.ks + r * D;
+    if (r < nq) return static_cast<const T*>(A.q) + t * A.qs + (r - nk) * D;
+    return static_cast<const T*>(A.v) + t * A.vs + (r - nq) * D;
+  };
+  auto dst = [&](int r) -> T* {
+    if (r < nk) return static_cast<T*>(A.k_cache) + static_cast<size_t>(row + static_cast<long long>(r) * A.ps) * D;
+    if (r < nq) return static_cast<T*>(A.q_out) + (t * A.Hq + (r - nk)) * D;
+    return static_cast<T*>(A.v_cache) + static_cast<size_t>(row + static_cast<long long>(r - nq) * A.ps) * D;
+  };
+  for (int r = r0; r < rows; r += kUnroll * A.lanes) {
+    Chunk<T, E> ca[kUnroll], cb[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; k++) {
+      const int h = r + k * A.lanes;
+      if (h >= rows) break;
+      const T* x = src(h);
+      ca[k].load(x + P.a);
+      cb[k].load(x + P.b);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; k++) {
+      const int h = r + k * A.lanes;
+      if (h >= rows) break;
+      if (P.turned && h < nq) P.apply(ca[k], cb[k]);
+      T* o = dst(h);
+      ca[k].store(o + P.a);
+      cb[k].store(o + P.b);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+// Threads that share a token's rows and tokens of a block. As many threads per
+// token as it takes to put about `want` threads on the device, a power of two,
+// at most one per row: a thread with more rows computes its cosines for more
+// rows, and issues the loads of kUnroll of them together.
+struct Split {
+  int lanes, tok_block, row_y;
+};
+Split split_rows(long long tokens, int rows, int np, int sms) {
+  const long long want = 1024LL * sms;
+  int lanes = 1;
+  while (lanes < rows && lanes < 4096 && tokens * np * lanes < want) lanes *= 2;
+  Split s;
+  const int per = kThreads / np;  // (token, lane) places of a block
+  const int hl = std::min(lanes, per);
+  s.tok_block = std::min(per / hl, kMaxTok);
+  const int hl2 = per / s.tok_block;
+  s.row_y = std::max(1, lanes / hl2);
+  s.lanes = s.row_y * hl2;
+  return s;
+}
+
+bool plan_ok(const vattn_rope* r) {
+  return r && (r->head_dim == 64 || r->head_dim == 128) && r->rot_dim >= 2 && r->rot_dim <= r->head_dim &&
+         r->rot_dim % 2 == 0 && (r->layout == VATTN_ROPE_HALF || r->layout == VATTN_ROPE_INTERLEAVED) &&
+         r->amplitude > 0.0f && isfinite(r->amplitude);
+}
+
+template <typename A>
+int launch_rows(void (*kern)(A), unsigned gx, unsigned gy, const A& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(gx, gy);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? VATTN_OK : VATTN_ECUDA;
+}
+
+template <typename T, int D>
+int run_rotate(RotateArgs& a, bool vec, int sms, cudaStream_t st) {
+  constexpr int E = 16 / sizeof(T);
+  const int np = vec ? D / (2 * E) : D / 2;
+  const Split s = split_rows(a.tokens, a.heads, np, sms);
+  a.lanes = s.lanes;
+  a.tok_block = s.tok_block;
+  const unsigned gx = static_cast<unsigned>((a.tokens + s.tok_block - 1) / s.tok_block);
+  return launch_rows(vec ? k_rotate<T, D, E> : k_rotate<T, D, 1>, gx, static_cast<unsigned>(s.row_y), a, st);
+}
+
+template <typename T, int D, int PROXY>
+int run_append(AppendArgs& a, bool vec, int sms, cudaStream_t st) {
+  constexpr int E = 16 / sizeof(T);
+  const int np = vec ? D / (2 * E) : D / 2;
+  const int rows = a.Hkv * (PROXY == VATTN_EXACT ? 2 : 1) + (a.q ? a.Hq : 0);
+  const Split s = split_rows(a.tokens, rows, np, sms);
+  a.lanes = s.lanes;
+  a.tok_block = s.tok_block;
+  a.row_y = s.row_y;
+  a.key_blocks = 0;
+  if (PROXY != VATTN_EXACT) {
+    const long long tiles = (a.tokens + kKeyTile<T> - 1) / kKeyTile<T>;
+    if (tiles * a.Hkv > 0x3FFFFFFFLL) return VATTN_EINVAL;
+    a.key_blocks = static_cast<int>(tiles * a.Hkv);
+  }
+  const long long gx = a.key_blocks + static_cast<long long>((a.tokens + s.tok_block - 1) / s.tok_block) * s.row_y;
+  if (gx > 0x7FFFFFFFLL) return VATTN_EINVAL;
+  return launch_rows(vec ? k_append<T, D, E, PROXY> : k_append<T, D, 1, PROXY>, static_cast<unsigned>(gx), 1u, a, st);
+}
+
+template <typename T, int D>
+int run_append(AppendArgs& a, int proxy, bool vec, int sms, cudaStream_t st) {
+  if (proxy == VATTN_SPARQ) return run_append<T, D, VATTN_SPARQ>(a, vec, sms, st);
+  if (proxy == VATTN_LOKI) return run_append<T, D, VATTN_LOKI>(a, vec, sms, st);
+  return run_append<T, D, VATTN_EXACT>(a, vec, sms, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int vattn_rope_init(vattn_rope* rope, const vattn_rope_config* cfg) {
+  if (!rope || !cfg) return VATTN_EINVAL;
+  const vattn_rope_config& c = *cfg;
+  if (!(c.head_dim == 64 || c.head_dim == 128)) return VATTN_EINVAL;
+  if (c.rot_dim < 2 || c.rot_dim > c.head_dim || c.rot_dim % 2) return VATTN_EINVAL;
+  if (c.layout != VATTN_ROPE_HALF && c.layout != VATTN_ROPE_INTERLEAVED) return VATTN_EINVAL;
+  if (c.scaling < VATTN_ROPE_NONE || c.scaling > VATTN_ROPE_YARN) return VATTN_EINVAL;
+  if (!(c.base > 1.0) || !isfinite(c.base)) return VATTN_EINVAL;
+  if (!(c.amplitude >= 0.0) || !isfinite(c.amplitude)) return VATTN_EINVAL;
+  if (c.scaling != VATTN_ROPE_NONE && (!(c.factor > 0.0) || !isfinite(c.factor))) return VATTN_EINVAL;
+  const bool by_ctx = c.scaling == VATTN_ROPE_BANDS || c.scaling == VATTN_ROPE_YARN;
+  if (by_ctx && (!(c.original_ctx > 0.0) || !isfinite(c.original_ctx))) return VATTN_EINVAL;
+  if (c.scaling == VATTN_ROPE_BANDS && !(c.low > 0.0 && c.low < c.high && isfinite(c.high))) return VATTN_EINVAL;
+  if (c.scaling == VATTN_ROPE_YARN && !(c.slow > 0.0 && c.slow < c.fast && isfinite(c.fast))) return VATTN_EINVAL;
+  const long double two_pi = 6.283185307179586476925286766559L;
+  const int r = c.rot_dim;
+  long double base = c.base;
+  if (c.scaling == VATTN_ROPE_BASE && r > 2)
+    base *= powl(c.factor, static_cast<long double>(r) / (r - 2));
+  if (!(base > 1.0L) || !isfinite(static_cast<double>(base))) return VATTN_EINVAL;
+  auto corner = [&](double n) { return r * logl(c.original_ctx / (n * two_pi)) / (2.0L * logl(c.base)); };
+  long double lo = 0.0L, span = 1.0L;
+  if (c.scaling == VATTN_ROPE_YARN) {
+    lo = fmaxl(floorl(corner(c.fast)), 0.0L);
+    const long double hi = fminl(ceill(corner(c.slow)), static_cast<long double>(r - 1));
+    span = hi > lo ? hi - lo : 0.001L;
+  }
+  vattn_rope out = {};
+  out.head_dim = c.head_dim;
+  out.rot_dim = r;
+  out.layout = c.layout;
+  double amp = c.amplitude;
+  if (amp == 0.0) amp = c.scaling == VATTN_ROPE_YARN && c.factor > 1.0 ? 0.1 * log(c.factor) + 1.0 : 1.0;
+  out.amplitude = static_cast<float>(amp);
+  if (!(out.amplitude > 0.0f) || !isfinite(out.amplitude)) return VATTN_EINVAL;
+  for (int i = 0; i < r / 2; i++) {
+    long double f = powl(base, -2.0L * i / r);
+    if (c.scaling == VATTN_ROPE_LINEAR) {
+      f /= c.factor;
+    } else if (c.scaling == VATTN_ROPE_BANDS) {
+      const long double t = (c.original_ctx * f / two_pi - c.low) / (c.high - c.low);
+      const long double keep = fminl(fmaxl(t, 0.0L), 1.0L);
+      f = keep * f + (1.0L - keep) * f / c.factor;
+    } else if (c.scaling == VATTN_ROPE_YARN) {
+      const long double ramp = fminl(fmaxl((i - lo) / span, 0.0L), 1.0L);
+      f = f * (1.0L - ramp) + f / c.factor * ramp;
+    }
+    const long double turns = fmodl(f / two_pi, 1.0L);
+    // below 2^64: turns < 1; a value that rounds up to a whole turn is turn 0
+    const long double scaled = rintl(turns * 18446744073709551616.0L);
+    out.turns[i] = scaled >= 18446744073709551616.0L ? 0ull : static_cast<uint64_t>(scaled);
+  }
+  *rope = out;
+  return VATTN_OK;
+}
+
+int vattn_rotate(const vattn_rope* rope, const void* x, void* out, const int32_t* positions, int tokens, int heads,
+                 int dtype, long long xt, long long xh, long long ot, long long oh, int transpose, void* stream) {
+  if (!plan_ok(rope) || tokens < 0 || tokens > kMaxTokens || heads < 0 || heads > kMaxHeads) return VATTN_EINVAL;
+  if (dtype != VATTN_FP32 && dtype != VATTN_BF16) return VATTN_EINVAL;
+  if (tokens == 0 || heads == 0) return VATTN_OK;
+  if (!x || !out || !positions) return VATTN_EINVAL;
+  const int D = rope->head_dim;
+  if (xt < 0 || xh < 0 || ot < 0 || oh < 0) return VATTN_EINVAL;
+  if (heads > 1 && oh < D) return VATTN_EINVAL;
+  if (tokens > 1 && ot < (heads - 1) * oh + D) return VATTN_EINVAL;
+  if (x == out && ((tokens > 1 && xt != ot) || (heads > 1 && xh != oh))) return VATTN_EINVAL;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return VATTN_ECUDA;
+  RotateArgs a;
+  a.rope = *rope;
+  a.x = x;
+  a.out = out;
+  a.positions = positions;
+  a.tokens = tokens;
+  a.heads = heads;
+  a.transpose = transpose;
+  a.xt = tokens > 1 ? xt : 0;
+  a.xh = heads > 1 ? xh : 0;
+  a.ot = tokens > 1 ? ot : 0;
+  a.oh = heads > 1 ? oh : 0;
+  // 16-byte chunks where every chunk of every row is aligned and no chunk
+  // crosses the end of the rotated part
+  const int E = dtype == VATTN_BF16 ? 8 : 4;
+  const bool vec = rope->rot_dim / 2 % E == 0 && aligned16(x) && aligned16(out) &&
+                   (a.xt | a.xh | a.ot | a.oh) % E == 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == VATTN_BF16)
+    return D == 128 ? run_rotate<__nv_bfloat16, 128>(a, vec, sms, st) : run_rotate<__nv_bfloat16, 64>(a, vec, sms, st);
+  return D == 128 ? run_rotate<float, 128>(a, vec, sms, st) : run_rotate<float, 64>(a, vec, sms, st);
+}
+
+int vattn_append(vattn_ctx* ctx, const vattn_append_params* prm, const int32_t* page_table, const int32_t* seq_lens,
+                 int batch, void* stream) {
+  if (!ctx) return VATTN_EINVAL;
+  ctx->last_status = VATTN_EINVAL;
+  const vattn_config& c = ctx->cfg;
+  const int D = c.head_dim;
+  if (!prm || batch < 0 || batch > c.max_batch || prm->tokens < 0 || prm->tokens > kMaxTokens || prm->num_pages < 1) return VATTN_EINVAL;
+  if (prm->rope && (!plan_ok(prm->rope) || prm->rope->head_dim != D)) return VATTN_EINVAL;
+  if (!prm->cu_tokens && prm->tokens != batch) return VATTN_EINVAL;
+  if (static_cast<unsigned long long>(prm->num_pages) * c.num_kv_heads * static_cast<unsigned long long>(c.page_size) >
+      0x7FFFFFFFull)
+    return VATTN_EINVAL;
+  if (batch == 0 || prm->tokens == 0) {
+    ctx->last_launches = 0;
+    return ctx->last_status = VATTN_OK;
+  }
+  if (!page_table || !seq_lens || !prm->k || !prm->v || !prm->k_cache || !prm->v_cache) return VATTN_EINVAL;
+  if (prm->q && !prm->q_out) return VATTN_EINVAL;
+  const long long kvw = static_cast<long long>(c.num_kv_heads) * D, qw = static_cast<long long>(c.num_q_heads) * D;
+  if (prm->k_stride < kvw || prm->v_stride < kvw) return VATTN_EINVAL;
+  if (prm->q && (prm->q_stride < qw || (prm->q == prm->q_out && prm->q_stride != qw))) return VATTN_EINVAL;
+  if (!aligned16(prm->k_cache) || !aligned16(prm->v_cache)) return VATTN_EINVAL;
+  if (c.proxy == VATTN_SPARQ && (!prm->k_t_cache || !aligned16(prm->k_t_cache))) return VATTN_EINVAL;
+  if (c.proxy == VATTN_LOKI && (!prm->k_proj_cache || !prm->proj_basis || !aligned16(prm->k_proj_cache)))
+    return VATTN_EINVAL;
+  AppendArgs a = {};
+  const void *kc = prm->k_cache, *vc = prm->v_cache;
+  if (const int rc = vattn::cache_ptrs(c, &kc, &vc)) return ctx->last_status = rc;
+  if (prm->rope) a.rope = *prm->rope;
+  a.k = prm->k;
+  a.v = prm->v;
+  a.q = prm->q;
+  a.ks = prm->k_stride;
+  a.vs = prm->v_stride;
+  a.qs = prm->q_stride;
+  a.q_out = prm->q_out;
+  a.k_cache = const_cast<void*>(kc);
+  a.v_cache = const_cast<void*>(vc);
+  a.k_t = prm->k_t_cache;
+  a.k_proj = prm->k_proj_cache;
+  a.basis = prm->proj_basis;
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.cu = prm->cu_tokens;
+  a.err = ctx->err;
+  a.tokens = prm->tokens;
+  a.batch = batch;
+  a.Hq = c.num_q_heads;
+  a.Hkv = c.num_kv_heads;
+  a.ps = c.page_size;
+  a.pps = (c.max_ctx + c.page_size - 1) / c.page_size;
+  a.max_ctx = c.max_ctx;
+  a.num_pages = prm->num_pages;
+  const int E = c.dtype == VATTN_BF16 ? 8 : 4;
+  const bool vec = a.rope.rot_dim / 2 % E == 0 && aligned16(a.k) && aligned16(a.v) && (a.ks | a.vs) % E == 0 &&
+                   (!a.q || (aligned16(a.q) && aligned16(a.q_out) && a.qs % E == 0));
+  vattn::DeviceScope scope(ctx->device);
+  if (!scope.ok) return ctx->last_status = VATTN_ECUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int rc;
+  if (c.dtype == VATTN_BF16)
+    rc = D == 128 ? run_append<__nv_bfloat16, 128>(a, c.proxy, vec, ctx->num_sms, st)
+                  : run_append<__nv_bfloat16, 64>(a, c.proxy, vec, ctx->num_sms, st);
+  else
+    rc = D == 128 ? run_append<float, 128>(a, c.proxy, vec, ctx->num_sms, st)
+                  : run_append<float, 64>(a, c.proxy, vec, ctx->num_sms, st);
+  ctx->last_launches = rc == VATTN_OK ? 1 : 0;
+  return ctx->last_status = rc;
+}
+
+}  // extern "C"

@@ -516,7 +516,9 @@ __device__ __forceinline__ int tail_position(const int* topk, int k, int s1, int
 //   sample: part 0 = the whole tail when the budget covers it; part 1 = the
 //           draws t in [p, b).
 //   dense:  part 0 = every position.
-constexpr int kModeDet = 0, kModeSample = 1, kModeDense = 2;
+// kModeSuffix: dense over positions [inf.s1, inf.n) (the part of a sequence
+// behind a shared prefix)
+constexpr int kModeDet = 0, kModeSample = 1, kModeDense = 2, kModeSuffix = 3;
 
 // Each warp streams its blocks of R rows through a private ring of NS
 // shared-memory stages: one lane per row issues two bulk copies (the K row
@@ -607,7 +609,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity, int tr
 // async-proxy writes (a bulk copy into a stage that was just read).
 // Bounded waits for blocks [t, nis) of a slice (ring stage and phase from
 // the running block count issued + t), after the wait on block t failed.
-__device__ __noinline__ void drain_ring(uint64_t* bars, int NS, unsigned issued, int t, int nis) {
+static __device__ __noinline__ void drain_ring(uint64_t* bars, int NS, unsigned issued, int t, int nis) {
   for (int t2 = t; t2 < nis; t2++) {
     const unsigned g = issued + static_cast<unsigned>(t2);
     mbar_wait(&bars[g % NS], (g / NS) & 1u);
@@ -1026,7 +1028,7 @@ __device__ void find_mass_digit(const unsigned long long* hm, const unsigned* hc
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kToppThreads, 1) k_topp(DevParams P) {
+static __global__ void __launch_bounds__(kToppThreads, 1) k_topp(DevParams P) {
   __shared__ unsigned long long s_hm[kHist1];
   __shared__ unsigned s_hc[kHist1];
   __shared__ unsigned long long s_w[32];
@@ -1580,6 +1582,7 @@ __global__ void __launch_bounds__(GatherShape<T, D, G>::NW * 32, 1) k_gather(con
       const int x = t * R + lane;
       if (t >= nbw || lane >= R || x >= nitems) return -1;
       if (MODE == kModeDense) return lb + x;
+      if (MODE == kModeSuffix) return inf.s1 + lb + x;
       const int i = item_of(x);
       if (MODE == kModeDet && part == 0) {  // sinks and window follow from the regions
         if (i < inf.s1) return i;
@@ -1958,7 +1961,7 @@ __global__ void __launch_bounds__(TcShape<D, G>::NW * 32, 1) k_gather_tc(const _
   using S = TcShape<D, G>;
   constexpr int R = S::R, H = S::H, HALF = S::HALF, MATB = S::MATB, BLKB = S::BLKB, NW = S::NW, NS = S::NS,
                 KT = S::KT, REC = S::REC;
-  static_assert(MODE == kModeSample || MODE == kModeDense, "sample and dense gathers");
+  static_assert(MODE == kModeSample || MODE == kModeDense || MODE == kModeSuffix, "sample and dense gathers");
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -2036,6 +2039,7 @@ __global__ void __launch_bounds__(TcShape<D, G>::NW * 32, 1) k_gather_tc(const _
       const int x = t * R + lane;
       if (t >= nbw || lane >= R || x >= nitems) return -1;
       if (MODE == kModeDense) return lb + x;
+      if (MODE == kModeSuffix) return inf.s1 + lb + x;
       return sel[inf.nI + (whole_tail ? lb + x : inf.p + lb + x)];
     };
     auto pid_of = [&](int pos) -> int {
@@ -2194,7 +2198,7 @@ __global__ void __launch_bounds__(TcShape<D, G>::NW * 32, 1) k_gather_tc(const _
 // tail, draw t is the Lemire map of Philox word t onto the tail; when the tail
 // is taken whole, entry t is the t-th tail position. Written to
 // sel[nI + t]. The sorted top-k list is staged in s_topk when it fits.
-__device__ void write_draw_positions(const DevParams& P, int u, const UnitInfo& inf, bool whole_tail,
+static __device__ void write_draw_positions(const DevParams& P, int u, const UnitInfo& inf, bool whole_tail,
                                      int t0, int t1, int* s_topk) {
   const int* g = P.sel + static_cast<size_t>(u) * P.max_ctx + inf.s1;
   const int* topk = g;
@@ -2496,7 +2500,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_topk(DevParams P) {
 // Positions of the sample's entries after the budget: draws t in [p, b), or
 // the whole tail when the budget covers it; CTA (0, 0) also writes the sample
 // gather's slice prefix (every budget is known by now). Grid (units, splits).
-__global__ void __launch_bounds__(128) k_draws(DevParams P) {
+static __global__ void __launch_bounds__(128) k_draws(DevParams P) {
   __shared__ int s_topk[kTopkSmem];
   grid_dependency_wait();
   if (blockIdx.x == 0 && blockIdx.y == 0) {
@@ -2717,7 +2721,7 @@ __global__ void __launch_bounds__(kCombWarps * 32, 2) k_combine(DevParams P) {
 // bytes that no copy ever delivers (no copy is issued, so nothing is in
 // flight at exit), waits with a limit of `tries`, and on timeout sets
 // VATTN_DEV_TIMEOUT in the error word, exactly as the copy rings do.
-__global__ void __launch_bounds__(32) k_wait_check(unsigned* err, int tries) {
+static __global__ void __launch_bounds__(32) k_wait_check(unsigned* err, int tries) {
   __shared__ __align__(8) uint64_t s_bar;
   if (threadIdx.x == 0) {
     mbar_init(&s_bar, 1);

@@ -1,0 +1,140 @@
+// Host side of vattn_shared_dense_decode.
+#include <algorithm>
+#include <type_traits>
+
+#include "vattn_ctx.h"
+#include "vattn_shared.cuh"
+
+using vattn::DevParams;
+using vattn::SharedParams;
+
+namespace {
+
+struct SharedKernels {
+  void (*prefix)(SharedParams);
+  int RB, KT, split;
+  unsigned threads;
+  size_t smem;
+  void (*own)(DevParams);   // the gather of the sequences' own positions
+  unsigned own_threads;
+  size_t own_smem;
+  void (*combine)(SharedParams);
+};
+
+template <typename T, int D, int G>
+SharedKernels kernels_for(bool host_kv) {
+  using vattn::kModeSuffix;
+  SharedKernels k;
+  k.prefix = vattn::k_shared_prefix<T, D>;
+  k.RB = vattn::PrefixShape<D>::RB;
+  k.KT = vattn::PrefixShape<D>::KT;
+  k.split = 0;
+  k.threads = 256;
+  k.smem = vattn::PrefixShape<D>::SMEM;
+  k.own = host_kv ? vattn::k_gather<T, D, G, kModeSuffix, true> : vattn::k_gather<T, D, G, kModeSuffix>;
+  k.own_smem = vattn::GatherShape<T, D, G>::SMEM;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    if (!host_kv) {
+      k.own = vattn::k_gather_tc<D, G, kModeSuffix>;
+      k.own_smem = vattn::TcShape<D, G>::SMEM;
+    }
+  }
+  k.own_threads = vattn::GatherShape<T, D, G>::NW * 32;
+  k.combine = vattn::k_shared_combine<D>;
+  return k;
+}
+
+template <typename T, int D>
+SharedKernels pick_g(int G, bool host_kv) {
+  if (G == 1) return kernels_for<T, D, 1>(host_kv);
+  if (G == 2) return kernels_for<T, D, 2>(host_kv);
+  if (G == 4) return kernels_for<T, D, 4>(host_kv);
+  return kernels_for<T, D, 8>(host_kv);
+}
+
+SharedKernels pick(const vattn_ctx* ctx) {
+  const vattn_config& c = ctx->cfg;
+  const bool host_kv = c.kv_location == VATTN_KV_HOST;
+  if (c.dtype == VATTN_BF16)
+    return c.head_dim == 128 ? pick_g<__nv_bfloat16, 128>(ctx->G, host_kv) : pick_g<__nv_bfloat16, 64>(ctx->G, host_kv);
+  return c.head_dim == 128 ? pick_g<float, 128>(ctx->G, host_kv) : pick_g<float, 64>(ctx->G, host_kv);
+}
+
+}  // namespace
+
+namespace vattn {
+
+size_t shared_workspace(vattn_ctx* ctx, char* p) {
+  const vattn_config& c = ctx->cfg;
+  const SharedKernels k = pick(ctx);
+  const size_t B = static_cast<size_t>(c.max_batch);
+  // one block's rows per CTA for segments that a CTA's end cuts, and every
+  // block's rows once (twice in a block that keeps two records a row)
+  const size_t rows = static_cast<size_t>(ctx->num_sms) * k.RB + (k.split ? 2 : 1) * B * c.num_q_heads;
+  const size_t sz_int = align256(B * sizeof(int)), sz_sum = align256((B + 1) * sizeof(long long));
+  const size_t sz_rec = align256(rows * c.head_dim * sizeof(float)), sz_ml = align256(rows * sizeof(float2));
+  if (p) {
+    SharedWork& w = ctx->shared;
+    w.reach = reinterpret_cast<int*>(p); p += sz_int;
+    w.pages_ok = reinterpret_cast<int*>(p); p += sz_int;
+    w.tiles = reinterpret_cast<long long*>(p); p += sz_sum;
+    w.rows = reinterpret_cast<long long*>(p); p += sz_sum;
+    w.rec = reinterpret_cast<float*>(p); p += sz_rec;
+    w.ml = reinterpret_cast<float2*>(p);
+    w.grid = ctx->num_sms;
+    cudaFuncSetAttribute(k.prefix, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
+    cudaFuncSetAttribute(k.own, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.own_smem));
+  }
+  return 2 * sz_int + 2 * sz_sum + sz_rec + sz_ml;
+}
+
+}  // namespace vattn
+
+extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* page_table, const int32_t* seq_lens,
+                                         const int32_t* group_start, const int32_t* prefix_lens, int groups, int batch,
+                                         int num_pages, float* out, void* stream) {
+  if (!ctx) return VATTN_EINVAL;
+  ctx->last_status = VATTN_EINVAL;
+  const vattn_config& c = ctx->cfg;
+  if (batch < 0 || batch > c.max_batch || groups < 0 || groups > batch || num_pages < 1) return VATTN_EINVAL;
+  if (batch > 0 && groups == 0) return VATTN_EINVAL;
+  if (batch == 0) {
+    ctx->last_launches = 0;
+    return ctx->last_status = VATTN_OK;
+  }
+  if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !group_start || !prefix_lens || !out)
+    return VATTN_EINVAL;
+  if (!vattn::aligned16(q) || !vattn::aligned16(k_cache) || !vattn::aligned16(v_cache)) return VATTN_EINVAL;
+  vattn::DeviceScope scope(ctx->device);
+  if (!scope.ok) return ctx->last_status = VATTN_ECUDA;
+  SharedParams P;
+  vattn::fill_common(ctx, &P.D, batch);
+  P.D.num_pages = num_pages;
+  P.D.dense = 1;
+  P.D.proxy = VATTN_EXACT;
+  if (const int rc = vattn::cache_ptrs(c, &k_cache, &v_cache)) return ctx->last_status = rc;
+  if (!P.D.kv_host)
+    if (const int rc = vattn::encode_row_maps(c, k_cache, v_cache, num_pages, &P.D)) return ctx->last_status = rc;
+  P.D.q = q;
+  P.D.k = k_cache;
+  P.D.v = v_cache;
+  P.D.page_table = page_table;
+  P.D.seq_lens = seq_lens;
+  P.D.out = out;
+  const SharedKernels k = pick(ctx);
+  P.W = ctx->shared;
+  P.group_start = group_start;
+  P.prefix_lens = prefix_lens;
+  P.groups = groups;
+  P.RB = k.RB;
+  P.KT = k.KT;
+  P.split = k.split;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int launches = 0;
+  vattn::launch(vattn::k_shared_prep, dim3(batch + groups + 1), dim3(vattn::kSharedPrepThreads), 0, st, P, &launches);
+  vattn::launch(k.prefix, dim3(ctx->num_sms), dim3(k.threads), k.smem, st, P, &launches);
+  vattn::launch(k.own, dim3(ctx->gather_grid), dim3(k.own_threads), k.own_smem, st, P.D, &launches);
+  vattn::launch(k.combine, dim3(P.D.units, ctx->G), dim3(vattn::kSharedCombWarps * 32), 0, st, P, &launches);
+  return vattn::finish(ctx, launches);
+}
