@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(HERE, f) for f in ("vattn_api.cu", "vattn_static.cu", "vattn_append.cu", "vattn_shared.cu")]
-DEPS = [*SRCS, *(os.path.join(HERE, f) for f in ("vattn_kernels.cuh", "vattn_device.cuh", "vattn_ctx.h", "vattn_shared.cuh")),
+DEPS = [*SRCS, *(os.path.join(HERE, f) for f in ("vattn_kernels.cuh", "vattn_device.cuh", "vattn_ctx.h", "vattn_shared.cuh", "vattn_prefix_tc.cuh")),
         os.path.join(ROOT, "include", "vattn.h")]
 OUT = os.path.join(PKG, "libvattn.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -4,6 +4,7 @@
 
 #include "vattn_ctx.h"
 #include "vattn_shared.cuh"
+#include "vattn_prefix_tc.cuh"
 
 using vattn::DevParams;
 using vattn::SharedParams;
@@ -35,6 +36,12 @@ SharedKernels kernels_for(bool host_kv) {
   k.own_smem = vattn::GatherShape<T, D, G>::SMEM;
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
     if (!host_kv) {
+      k.prefix = vattn::k_shared_prefix_tc<D>;
+      k.RB = 2 * vattn::PrefixTcShape<D>::M;
+      k.KT = vattn::PrefixTcShape<D>::KT;
+      k.split = 1;
+      k.threads = vattn::PrefixTcShape<D>::THREADS;
+      k.smem = vattn::PrefixTcShape<D>::SMEM;
       k.own = vattn::k_gather_tc<D, G, kModeSuffix>;
       k.own_smem = vattn::TcShape<D, G>::SMEM;
     }
@@ -50,6 +57,33 @@ SharedKernels pick_g(int G, bool host_kv) {
   if (G == 2) return kernels_for<T, D, 2>(host_kv);
   if (G == 4) return kernels_for<T, D, 4>(host_kv);
   return kernels_for<T, D, 8>(host_kv);
+}
+
+// The maps of the tensor-core prefix kernel.
+int encode_tile_maps(const vattn_config& c, int G, const void* q, const void* k, const void* v, int batch,
+                     int num_pages, SharedParams* P) {
+  const vattn::EncodeTiledFn fn = vattn::encode_tiled();
+  if (!fn) return VATTN_ECUDA;
+  int box = P->KT;
+  while (c.page_size % box) box /= 2;  // the page size is a multiple of 16
+  P->box = box;
+  const cuuint64_t d = static_cast<cuuint64_t>(c.head_dim);
+  const cuuint64_t rows = static_cast<cuuint64_t>(num_pages) * c.num_kv_heads * static_cast<cuuint64_t>(c.page_size);
+  const cuuint64_t dims[2] = {d, rows}, strides[1] = {2 * d};
+  const cuuint32_t boxes[2] = {64u, static_cast<cuuint32_t>(box)}, one[3] = {1u, 1u, 1u};
+  for (int i = 0; i < 2; i++)
+    if (fn(i ? &P->tmv_t : &P->tmk_t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(i ? v : k), dims, strides,
+           boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return VATTN_ECUDA;
+  const cuuint64_t Hq = static_cast<cuuint64_t>(c.num_q_heads);
+  const cuuint64_t qd[3] = {d, Hq, static_cast<cuuint64_t>(batch)}, qs[2] = {2 * d, 2 * d * Hq};
+  const cuuint32_t qb[3] = {64u, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(128 / G)};
+  if (fn(&P->tmq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), qd, qs, qb, one,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return VATTN_ECUDA;
+  return VATTN_OK;
 }
 
 SharedKernels pick(const vattn_ctx* ctx) {
@@ -130,6 +164,9 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
   P.RB = k.RB;
   P.KT = k.KT;
   P.split = k.split;
+  if (k.split)
+    if (const int rc = encode_tile_maps(c, ctx->G, q, k_cache, v_cache, batch, num_pages, &P))
+      return ctx->last_status = rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int launches = 0;
   vattn::launch(vattn::k_shared_prep, dim3(batch + groups + 1), dim3(vattn::kSharedPrepThreads), 0, st, P, &launches);

@@ -3,7 +3,7 @@
 //
 //   k_shared_prep     validates lengths, groups and pages; the work of the
 //                     prefix kernel and of the gather as prefix sums
-//   k_shared_prefix   every group's prefix against all of its queries
+//   k_shared_prefix(_tc)  every group's prefix against all of its queries
 //   k_gather(_tc)<kModeSuffix>  every sequence's own positions
 //   k_shared_combine  merges the records of both parts
 //
@@ -27,6 +27,10 @@ constexpr unsigned kDevBadSeqlen = VATTN_DEV_BAD_SEQLEN, kDevBadPage = VATTN_DEV
                    kDevBadGroup = VATTN_DEV_BAD_GROUP;
 
 struct SharedParams {
+  // tensor-core prefix kernel: the caches in boxes of `box` rows by 64 columns,
+  // the queries [batch][Hq][d] in boxes of 128 rows (128 / G sequences, the G
+  // heads of a KV head) by 64 columns, 128-byte swizzle
+  CUtensorMap tmk_t, tmv_t, tmq;
   DevParams D;
   SharedWork W;
   const int* group_start;
@@ -34,6 +38,7 @@ struct SharedParams {
   int groups;
   int RB, KT;  // rows of a block, keys of a tile
   int split;   // 1: blocks of at most RB / 2 rows keep two records a row
+  int box;     // rows of a cache box: a power of two that divides the page size, at most KT
 };
 
 // ---------------------------------------------------------------- groups
