@@ -12,12 +12,19 @@
 
 namespace vattn {
 
+// One group of a shared-prefix decode; record [groups] holds the totals.
+struct alignas(16) SharedGroup {
+  int b0, size;            // its sequences
+  int prefix;
+  int tiles;               // key tiles of the prefix (0: not shared)
+  long long tile0, row0;   // key tiles (of every row block and head) and record rows before it
+};
+
 // Workspace of the shared-prefix decode (see vattn_shared.cuh).
 struct SharedWork {
   int* reach = nullptr;           // [max_batch] per group: sequences that reach the prefix's end
   int* pages_ok = nullptr;        // [max_batch] per group: the prefix's pages are valid
-  long long* tiles = nullptr;     // [max_batch + 1] prefix sum of key tiles over groups
-  long long* rows = nullptr;      // [max_batch + 1] prefix sum of record rows over groups
+  SharedGroup* group = nullptr;   // [max_batch + 1]
   float* rec = nullptr;           // [record rows][D]
   float2* ml = nullptr;           // [record rows] (maximum in log2 units, weight sum)
   int grid = 0;                   // CTAs of the prefix kernel

@@ -7,19 +7,23 @@
 //   two query tiles: step 2j + i is query tile i against key tile j, so a K or
 //                    V tile in shared memory serves both;
 //   one query tile:  step t is key tile t, into accumulator t % 2; the two
-//                    accumulators leave two records per row.
+//                    accumulators are merged into one record at the end.
 // Steps alternate between two stages (S, O and a softmax warpgroup each), so
 // that the tensor cores work on one stage while the other's softmax runs.
-//   warps 0-3, 4-7  softmax of stage 0 and 1: thread = row (TMEM lane)
+//   warps 0-3, 4-7  softmax of stage 0 and 1: thread = row (TMEM lane); they
+//                   also clear the V rows behind the prefix's last key, so that
+//                   whatever the cache holds there meets its zero weights as
+//                   zeros, and write the records
 //   warp 8          producer: Q, K and V tiles by TMA, 128-byte swizzle, K and
 //                   V through a ring of NST tiles; K and V blocks of `box` rows,
 //                   each inside one page
-//   warp 9          issues the MMAs (one thread) and clears the V rows behind
-//                   the prefix's last key, so that whatever the cache holds
-//                   there meets its zero weights as zeros
-// TMEM (512 columns): S0, S1, O0, O1 of 128 each. The weights overwrite their
-// scores as two bf16 terms (hi = bf16(p), lo = bf16(p - hi), 2^-17 relative),
-// the A operand of two products with V: fp32 outputs keep fp32's accuracy from
+//   warp 9          one thread issues the MMAs. Few of them queue up in the
+//                   tensor core, so every cycle between two products of this
+//                   thread idles it: no warp-wide step stands there, and the
+//                   weights are handed over in two halves of 64 keys
+// TMEM (512 columns): S0, S1, O0, O1 of 128 each. The weights of 32 keys
+// overwrite their scores as two bf16 terms (hi = bf16(p), lo = bf16(p - hi),
+// 2^-17 relative; 16 columns each), the A operand of two products with V: fp32 outputs keep fp32's accuracy from
 // bf16 products. The running maximum moves only when a tile exceeds it by more
 // than 2^8 (weights stay below 2^8, far inside fp32 and bf16), so O is rarely
 // rescaled; by the time a tile's scores are read, the stage's previous product
@@ -38,8 +42,16 @@ struct PrefixTcShape {
   static constexpr int TILE = H * HALF;              // a Q, K or V tile
   static constexpr int NST = 160 * 1024 / TILE;      // ring tiles
   static constexpr int THREADS = 320;
-  static constexpr size_t SMEM = 1024 + static_cast<size_t>(2 + NST) * TILE;
-  static_assert(SMEM <= 226 * 1024, "shared memory of the prefix kernel");
+  static constexpr int GROUPS = 16;                  // groups whose records fit shared memory
+  struct Tail {
+    uint64_t full[NST], empty[NST], qfull, qfree, s[2], p[2][2], o[2], ofree, done;
+    unsigned tmem;
+    int ok[GROUPS];
+    SharedGroup group[GROUPS + 1];
+    float2 ml[2][128];
+  };
+  static constexpr size_t SMEM = static_cast<size_t>(2 + NST) * TILE + sizeof(Tail);
+  static_assert(SMEM <= 227 * 1024, "shared memory of the prefix kernel");
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -49,20 +61,35 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+// One thread of a converged warp, the same one every time (commits track the
+// MMAs of the thread that issues them).
+__device__ __forceinline__ bool elect_one() {
+  unsigned p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+// Shared-memory descriptors of 128-byte-swizzled tiles: the low word holds the
+// address and `lead`, the bytes between 64-column blocks of an operand whose
+// columns are its M or N side (unused where they are its K side); the high
+// word the 1024 bytes between 8-row groups, the version and the swizzle.
+__device__ __forceinline__ unsigned tc_desc_lo(unsigned addr, unsigned lead) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
+}
+constexpr unsigned kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 // D[tmem] (+)= A[smem] B[smem], bf16 operands, fp32 accumulation
-__device__ __forceinline__ void tc_mma_ss(unsigned d, uint64_t a, uint64_t b, unsigned idesc, bool accumulate) {
+__device__ __forceinline__ void tc_mma_ss(unsigned d, unsigned a, unsigned b, unsigned idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %4, 0;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(kDescHi)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void tc_mma_ts(unsigned d, unsigned a, uint64_t b, unsigned idesc, bool accumulate) {
+__device__ __forceinline__ void tc_mma_ts(unsigned d, unsigned a, unsigned b, unsigned idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.u32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(kDescHi)
       : "memory");
 }
 // this warp's 32 lanes x 32 columns from `t`: one row's columns per thread
@@ -74,6 +101,15 @@ __device__ __forceinline__ void tc_ld32(unsigned t, unsigned (&r)[32]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld16(unsigned t, unsigned (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(t)
       : "memory");
 }
@@ -103,13 +139,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Shared-memory descriptor of a 128-byte-swizzled tile: 8-row groups 1024 bytes
-// apart; `lead`: bytes between 64-column blocks of an operand whose columns are
-// its M or N side (unused where they are its K side).
-__device__ __forceinline__ uint64_t tc_desc(unsigned addr, unsigned lead) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
-}
 // Instruction descriptor: bf16 x bf16 -> fp32, M = 128, A by rows (K-major), B
 // by rows (K-major) or, with b_cols, with N contiguous.
 __host__ __device__ constexpr unsigned tc_idesc(int n, bool b_cols) {
@@ -132,8 +161,32 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x,
       : "memory");
 }
 
-// Steps of stage `st` in a segment.
-__device__ __forceinline__ int stage_steps(bool two, int nt, int st) { return two ? nt : (nt + 1 - st) / 2; }
+__device__ __forceinline__ float2 unpack_bf16x2(unsigned h) {
+  return make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
+}
+// 32 bytes in one store
+__device__ __forceinline__ void st_global_v8(float* p, const float (&x)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(p)), "f"(x[0]),
+               "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+
+// Scores from column nk on (of 64) become -inf.
+__device__ __forceinline__ void mask_tail(unsigned (&x)[2][32], int nk) {
+#pragma unroll
+  for (int k = 0; k < 2; k++)
+#pragma unroll
+    for (int j = 0; j < 32; j++)
+      if (32 * k + j >= nk) x[k][j] = __float_as_uint(-INFINITY);
+}
+__device__ __forceinline__ float max64(const unsigned (&x)[2][32]) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) m[i] = __uint_as_float(x[0][i]);
+#pragma unroll
+  for (int j = 4; j < 64; j++) m[j & 3] = fmaxf(m[j & 3], __uint_as_float(x[j / 32][j % 32]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
 
 constexpr float kRescale = 8.0f;  // log2 of the weights' bound before the maximum moves
 
@@ -142,47 +195,54 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
     k_shared_prefix_tc(const __grid_constant__ SharedParams P) {
   using S = PrefixTcShape<D>;
   constexpr int H = S::H, HALF = S::HALF, TILE = S::TILE, NST = S::NST, KT = S::KT;
-  extern __shared__ __align__(128) unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char* s_q = smem;
-  unsigned char* s_ring = smem + 2 * TILE;
-  __shared__ __align__(8) uint64_t b_full[NST], b_empty[NST], b_qfull, b_qfree, b_s[2], b_p[2], b_o[2], b_ofree[2],
-      b_done;
-  __shared__ unsigned s_tmem;
-  __shared__ int s_g;
+  extern __shared__ __align__(1024) unsigned char s_tiles[];  // the swizzle's pattern repeats every 1024 bytes
+  unsigned char* s_q = s_tiles;
+  unsigned char* s_ring = s_tiles + 2 * TILE;
+  typename S::Tail& tail = *reinterpret_cast<typename S::Tail*>(s_tiles + (2 + NST) * TILE);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; i++) {
-      mbar_init(&b_full[i], 1);
-      mbar_init(&b_empty[i], 1);
+      mbar_init(&tail.full[i], 1);
+      mbar_init(&tail.empty[i], 1);
     }
-    mbar_init(&b_qfull, 1);
-    mbar_init(&b_qfree, 1);
-    mbar_init(&b_done, 1);
+    mbar_init(&tail.qfull, 1);
+    mbar_init(&tail.qfree, 1);
+    mbar_init(&tail.ofree, 8);
+    mbar_init(&tail.done, 1);
     for (int i = 0; i < 2; i++) {
-      mbar_init(&b_s[i], 1);
-      mbar_init(&b_p[i], 4);
-      mbar_init(&b_o[i], 1);
-      mbar_init(&b_ofree[i], 4);
+      mbar_init(&tail.s[i], 1);
+      mbar_init(&tail.p[i][0], 4);
+      mbar_init(&tail.p[i][1], 4);
+      mbar_init(&tail.o[i], 1);
     }
-    s_g = 0;
     mbar_init_fence();
   }
+  if (warp == 8 && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &P.tmk_t : lane == 1 ? &P.tmv_t : &P.tmq) : "memory");
   if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tail.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
+  grid_dependency_wait();
+  // the groups' records, all at once
+  const bool cached = P.groups <= S::GROUPS;
+  if (cached) {
+    constexpr int W = sizeof(SharedGroup) / 16;
+    for (int i = threadIdx.x; i < (P.groups + 1) * W; i += S::THREADS)
+      reinterpret_cast<uint4*>(tail.group)[i] = reinterpret_cast<const uint4*>(P.W.group)[i];
+    for (int i = threadIdx.x; i < P.groups; i += S::THREADS) tail.ok[i] = P.W.pages_ok[i];
+  }
   __syncthreads();
   tc_fence_after();
-  const unsigned tmem = s_tmem;
-  grid_dependency_wait();
-
-  const long long Tt = P.W.tiles[P.groups];
+  const unsigned tmem = tail.tmem;
+  const SharedGroup* group = cached ? tail.group : P.W.group;
+  const int* pages_ok = cached ? tail.ok : P.W.pages_ok;
+  const long long Tt = group[P.groups].tile0;
   const long long beg = div_nonneg(Tt * blockIdx.x, gridDim.x), end = div_nonneg(Tt * (blockIdx.x + 1), gridDim.x);
-  const int gi0 = beg < end ? first_group(P, beg, &s_g) : 0;
+  int gi = group_at(P, group, beg);
   bool ok = true;
 
   if (warp == 8) {
@@ -191,181 +251,178 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
     const int blk = lane / H, hf = lane % H;
     unsigned li = 0;
     int seg = 0;
-    int gi = gi0;
     for (long long cur = beg; cur < end && ok;) {
-      const Segment s = segment_at(P, cur, end, gi);
+      const Segment s = segment_at(P, group, cur, end, gi);
       gi = s.gi;
       cur = s.next;
-      if (!P.W.pages_ok[s.gi]) continue;
-      const bool two = s.rows > 128;
-      // page of this lane's block of key tile t (position behind the prefix: no block)
-      const int* pages = P.D.page_table + static_cast<size_t>(s.g.b0) * P.D.pps;
+      if (!pages_ok[s.gi]) continue;
+      const int tiles_q = s.rows > 128 ? 2 : 1;
+      // first row of this lane's block of key tile t (-1: behind the prefix)
+      const int* pages = P.D.page_table + static_cast<size_t>(s.b0) * P.D.pps;
       auto row_of = [&](int t) -> int {
         const int pos = t * KT + blk * box;
-        if (t >= s.t1 || lane >= per || pos >= s.g.prefix) return -1;
+        if (t >= s.t1 || lane >= per || pos >= s.prefix) return -1;
         const int slot = page_slot(P.D, pos);
         return (pages[slot] * P.D.Hkv + s.h) * P.D.ps + (pos - slot * P.D.ps);
       };
       int row = row_of(s.t0);
-      if (seg > 0) ok = __all_sync(0xffffffffu, mbar_wait(&b_qfree, (seg - 1) & 1));
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&b_qfull, static_cast<unsigned>((two ? 2 : 1) * TILE));
-        const int b0 = s.g.b0 + s.row0 / P.D.G;
-        for (int t = 0; t < (two ? 2 : 1); t++)
-          for (int x = 0; x < H; x++)
-            tma_3d(s_q + t * TILE + x * HALF, &P.tmq, x * 64, s.h * P.D.G, b0 + t * (128 / P.D.G), &b_qfull);
-      }
-      seg++;
       for (int t = s.t0; t < s.t1 && ok; t++) {
         const int next = row_of(t + 1);
-        const int nblk = min(KT / box, (s.g.prefix - t * KT + box - 1) / box);
+        const int nblk = min(KT / box, (s.prefix - t * KT + box - 1) / box);
         for (int kv = 0; kv < 2; kv++, li++) {
           const unsigned st = li % NST;
-          if (li >= NST) ok = __all_sync(0xffffffffu, mbar_wait(&b_empty[st], (li / NST - 1) & 1u));
+          if (li >= NST) ok = __all_sync(0xffffffffu, mbar_wait(&tail.empty[st], (li / NST - 1) & 1u));
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&b_full[st], static_cast<unsigned>(nblk * box * D * 2));
+          if (lane == 0) mbar_arrive_expect_tx(&tail.full[st], static_cast<unsigned>(nblk * box * D * 2));
           __syncwarp();
           if (row >= 0)
             tma_2d(s_ring + st * TILE + hf * HALF + blk * box * 128, kv ? &P.tmv_t : &P.tmk_t, hf * 64, row,
-                   &b_full[st]);
+                   &tail.full[st]);
         }
         row = next;
+        if (t == s.t0 && ok) {
+          // the queries, once the segment before has computed its last scores
+          if (seg > 0) ok = __all_sync(0xffffffffu, mbar_wait(&tail.qfree, (seg - 1) & 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&tail.qfull, static_cast<unsigned>(tiles_q * TILE));
+          __syncwarp();
+          const int qt = lane / H;
+          if (qt < tiles_q)
+            tma_3d(s_q + qt * TILE + hf * HALF, &P.tmq, hf * 64, s.h * P.D.G,
+                   s.b0 + s.row0 / P.D.G + qt * (128 / P.D.G), &tail.qfull);
+          seg++;
+        }
       }
     }
     // no copy may land after the CTA has moved on (only after a failed wait are some still in flight)
-    if (!ok)
-      for (unsigned i = li > NST ? li - NST : 0; i < li; i++) mbar_wait(&b_full[i % NST], (i / NST) & 1u);
+    if (!ok) {
+      for (unsigned i = li > NST ? li - NST : 0; i < li; i++) mbar_wait(&tail.full[i % NST], (i / NST) & 1u);
+      if (seg > 0) mbar_wait(&tail.qfull, (seg - 1) & 1);
+    }
   } else if (warp == 9) {
-    // ------------------------------------------------------------ MMAs
-    constexpr unsigned kQK = tc_idesc(KT, false), kPV = tc_idesc(D, true);
-    const unsigned q_a = smem_u32(s_q), r_a = smem_u32(s_ring);
-    unsigned li0 = 0, np[2] = {0, 0}, no[2] = {0, 0};
-    int seg = 0, gi = gi0;
-    for (long long cur = beg; cur < end && ok;) {
-      const Segment s = segment_at(P, cur, end, gi);
-      gi = s.gi;
-      cur = s.next;
-      if (!P.W.pages_ok[s.gi]) continue;
-      const bool two = s.rows > 128;
-      const int nt = s.t1 - s.t0, n = two ? 2 * nt : nt;
-      auto qk = [&](int i) {
-        const int st = i & 1, kt = two ? i >> 1 : i;
-        const unsigned idx = li0 + 2u * kt, slot = idx % NST;
-        if (!two || st == 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&b_full[slot], (idx / NST) & 1u));
-        if (!ok) return;
-        tc_fence_after();
-        if (lane == 0) {
-          const unsigned a = q_a + (two ? st * TILE : 0), b = r_a + slot * TILE;
+    // ------------------------------------------------------------ MMAs, one thread
+    if (elect_one()) {
+      constexpr unsigned kQK = tc_idesc(KT, false), kPV = tc_idesc(D, true);
+      const unsigned q_d = tc_desc_lo(smem_u32(s_q), 16), k_d = tc_desc_lo(smem_u32(s_ring), 16),
+                     v_d = tc_desc_lo(smem_u32(s_ring), H > 1 ? HALF : 1024);
+      unsigned li0 = 0, np[2] = {0, 0};
+      int seg = 0;
+      for (long long cur = beg; cur < end && ok;) {
+        const Segment s = segment_at(P, group, cur, end, gi);
+        gi = s.gi;
+        cur = s.next;
+        if (!pages_ok[s.gi]) continue;
+        const bool two = s.rows > 128;
+        const int nt = s.t1 - s.t0, n = two ? 2 * nt : nt;
+        auto qk = [&](int i) {
+          const int st = i & 1, kt = two ? i >> 1 : i;
+          const unsigned idx = li0 + 2u * kt, slot = idx % NST;
+          if (!two || st == 0) ok = ok && mbar_wait(&tail.full[slot], (idx / NST) & 1u);
+          if (!ok) return;
+          tc_fence_after();
+          const unsigned a = q_d + (two ? st * (TILE >> 4) : 0), b = k_d + slot * (TILE >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; k++) {
-            const unsigned off = (k / 4) * HALF + (k % 4) * 32;
-            tc_mma_ss(tmem + st * 128, tc_desc(a + off, 16), tc_desc(b + off, 16), kQK, k > 0);
+            const unsigned off = ((k / 4) * HALF + (k % 4) * 32) >> 4;
+            tc_mma_ss(tmem + st * 128, a + off, b + off, kQK, k > 0);
           }
-          tc_commit(&b_s[st]);
-          if (!two || st == 1) tc_commit(&b_empty[slot]);
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int i) {
-        const int st = i & 1, kt = two ? i >> 1 : i;
-        const unsigned idx = li0 + 2u * kt + 1u, slot = idx % NST;
-        const bool first = two ? i < 2 : i == st;  // the stage's first step of the segment
-        const bool last = two ? i >= n - 2 : i + 2 >= n;
-        if (!two || st == 0) {
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&b_full[slot], (idx / NST) & 1u));
-          if (!ok) return;
-          const int nk = s.g.prefix - (s.t0 + kt) * KT;
-          if (nk < KT) {
-            for (int x = nk * 8 + lane; x < KT * 8; x += 32)
+          tc_commit(&tail.s[st]);
+          if (!two || st == 1) tc_commit(&tail.empty[slot]);
+        };
+        auto pv = [&](int i) {
+          const int st = i & 1, kt = two ? i >> 1 : i;
+          const unsigned idx = li0 + 2u * kt + 1u, slot = idx % NST;
+          const bool first = i < 2;  // the stage's first step of the segment
+          if (!two || st == 0) ok = ok && mbar_wait(&tail.full[slot], (idx / NST) & 1u);
+          // the accumulators of the segment before have been read
+          if (i == 0 && seg > 0) ok = ok && mbar_wait(&tail.ofree, (seg - 1) & 1);
+          const unsigned b = v_d + slot * (TILE >> 4), p = tmem + st * 128, o = tmem + 256 + st * 128;
 #pragma unroll
-              for (int hf = 0; hf < H; hf++)
-                *reinterpret_cast<uint4*>(s_ring + slot * TILE + hf * HALF + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async();
-            __syncwarp();
+          for (int half = 0; half < 2; half++) {
+            ok = ok && mbar_wait(&tail.p[st][half], np[st] & 1u);
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll
+            for (int term = 0; term < 2; term++)
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; k++)
+                tc_mma_ts(o, p + 32 * (k / 2) + 16 * term + 8 * (k % 2), b + (k * 2048 >> 4), kPV, k + term > 0 || !first);
           }
+          np[st]++;
+          if (!two || st == 1) tc_commit(&tail.empty[slot]);
+          if (i + 2 >= n) tc_commit(&tail.o[st]);  // the stage's last step
+        };
+        ok = mbar_wait(&tail.qfull, seg & 1);
+        if (!ok) break;
+        qk(0);
+        if (n > 1) qk(1);
+        if (n <= 2 && ok) tc_commit(&tail.qfree);
+        for (int i = 0; i < n && ok; i++) {
+          pv(i);
+          if (i + 2 < n && ok) qk(i + 2);
+          if (i + 3 == n && ok) tc_commit(&tail.qfree);  // the segment's last scores
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&b_p[st], np[st] & 1u));
-        np[st]++;
-        if (first && no[st] > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&b_ofree[st], (no[st] - 1) & 1u));
-        if (!ok) return;
-        tc_fence_after();
-        if (lane == 0) {
-          const unsigned b = r_a + slot * TILE, p = tmem + st * 128, o = tmem + 256 + st * 128;
-#pragma unroll
-          for (int term = 0; term < 2; term++)
-#pragma unroll
-            for (int k = 0; k < KT / 16; k++)
-              tc_mma_ts(o, p + term * 64 + k * 8, tc_desc(b + k * 2048, H > 1 ? HALF : 1024), kPV, !(first && term == 0 && k == 0));
-          if (!two || st == 1) tc_commit(&b_empty[slot]);
-          if (last) tc_commit(&b_o[st]);
-        }
-        __syncwarp();
-        if (last) no[st]++;
-      };
-      ok = __all_sync(0xffffffffu, mbar_wait(&b_qfull, seg & 1));
-      seg++;
-      if (!ok) break;
-      qk(0);
-      if (n > 1) qk(1);
-      for (int i = 0; i < n && ok; i++) {
-        pv(i);
-        if (i + 2 < n) qk(i + 2);
-        // the queries are free once the segment's last scores are computed
-        if (i == max(n - 3, 0) && ok && lane == 0) tc_commit(&b_qfree);
+        seg++;
+        li0 += 2u * nt;
       }
-      li0 += 2u * nt;
+      // every MMA and every arrival of a commit is complete before the CTA ends
+      tc_commit(&tail.done);
+      ok = mbar_wait(&tail.done, 0) && ok;
+      if (!ok) atomicOr(P.D.err, kDevTimeout);
     }
-    // every MMA and every arrival of a commit is complete before the CTA ends
-    if (lane == 0) tc_commit(&b_done);
     __syncwarp();
-    ok = __all_sync(0xffffffffu, mbar_wait(&b_done, 0)) && ok;
   } else {
     // ------------------------------------------------------------ softmax
     const int st = warp >> 2, quarter = warp & 3;
-    const unsigned sa = tmem + st * 128 + (static_cast<unsigned>(quarter * 32) << 16);
-    const unsigned oa = sa + 256;
+    const unsigned lanes = static_cast<unsigned>(quarter * 32) << 16;
+    const unsigned sa = tmem + st * 128 + lanes, oa = tmem + 256 + lanes;
     const float c = P.D.scale * 1.4426950408889634f;  // scores in log2 units
-    unsigned ns = 0, no = 0;
-    int gi = gi0;
+    const int r = quarter * 32 + lane;                // row of the query tile
+    unsigned ns = 0, no[2] = {0, 0}, li0 = 0;
     for (long long cur = beg; cur < end && ok;) {
-      const Segment s = segment_at(P, cur, end, gi);
+      const Segment s = segment_at(P, group, cur, end, gi);
       gi = s.gi;
       cur = s.next;
-      if (!P.W.pages_ok[s.gi]) continue;
+      if (!pages_ok[s.gi]) continue;
       const bool two = s.rows > 128;
-      const int steps = stage_steps(two, s.t1 - s.t0, st);
-      const int r = quarter * 32 + lane;                     // row of the query tile
-      const int valid = two ? s.rows - st * 128 : s.rows;    // its query rows
-      const bool idle = quarter * 32 >= valid;               // no query row in this warp
-      const long long row = s.rec + (two ? st * 128 : st * s.rows) + r;
+      const int nt = s.t1 - s.t0, steps = two ? nt : (nt + 1 - st) / 2;
+      const int valid = two ? s.rows - st * 128 : s.rows;  // query rows of the stage's tile
+      const bool idle = quarter * 32 >= valid;             // none in this warp
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < steps && ok; i++) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&b_s[st], ns & 1u));
+        const int kt = two ? i : 2 * i + st;
+        const int nk = s.prefix - (s.t0 + kt) * KT;
+        if (nk < KT && (!two || st == 0)) {
+          // the V rows behind the prefix's last key: zero, whatever the cache holds
+          const unsigned idx = li0 + 2u * kt + 1u, slot = idx % NST;
+          ok = __all_sync(0xffffffffu, mbar_wait(&tail.full[slot], (idx / NST) & 1u));
+          if (!ok) break;
+          for (int x = nk * 8 + r; x < KT * 8; x += 128)
+#pragma unroll
+            for (int hf = 0; hf < H; hf++)
+              *reinterpret_cast<uint4*>(s_ring + slot * TILE + hf * HALF + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async();
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&tail.s[st], ns & 1u));
         ns++;
         if (!ok) break;
         tc_fence_after();
+        // the row's 128 scores in four chunks of 32: the maximum over all; the
+        // first two stay in registers, the others are read again (their weights
+        // replace each chunk in place)
+        unsigned x[2][32];
+        float neg = 0.0f;
         if (!idle) {
-          unsigned x[4][32];
+          float top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 4; k++) tc_ld32(sa + 32 * k, x[k]);
-          tc_wait_ld();
-          const int nk = s.g.prefix - (two ? s.t0 + i : s.t0 + 2 * i + st) * KT;
-          if (nk < KT) {
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-#pragma unroll
-              for (int j = 0; j < 32; j++)
-                if (32 * k + j >= nk) x[k][j] = __float_as_uint(-INFINITY);
+          for (int k = 1; k >= 0; k--) {
+            tc_ld32(sa + 64 * k, x[0]);
+            tc_ld32(sa + 64 * k + 32, x[1]);
+            tc_wait_ld();
+            if (nk < KT) mask_tail(x, nk - 64 * k);
+            top = fmaxf(top, max64(x));
           }
-          float mx[4];
-#pragma unroll
-          for (int k = 0; k < 4; k++) {
-            mx[k] = __uint_as_float(x[k][0]);
-#pragma unroll
-            for (int j = 1; j < 32; j++) mx[k] = fmaxf(mx[k], __uint_as_float(x[k][j]));
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          top *= c;
           if (i == 0) {
             m = fmaxf(top, -1e30f);  // finite: scores of -inf weigh exactly 0
           } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
@@ -374,65 +431,102 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
             m = mn;
             l *= f;
 #pragma unroll 1
-            for (int k = 0; k < D / 32; k++) {
-              unsigned o[32];
-              tc_ld32(oa + 32 * k, o);
+            for (int k = 0; k < D / 16; k++) {
+              unsigned o[16];
+              tc_ld16(oa + st * 128 + 16 * k, o);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tc_st32(oa + 32 * k, o);
+              for (int j = 0; j < 16; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tc_st16(oa + st * 128 + 16 * k, o);
             }
           }
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int k = 0; k < 4; k++) {
-            unsigned hi[16], lo[16];
-#pragma unroll
-            for (int j = 0; j < 16; j++) {
-              const float p0 = ex2(fmaf(__uint_as_float(x[k][2 * j]), c, -m));
-              const float p1 = ex2(fmaf(__uint_as_float(x[k][2 * j + 1]), c, -m));
-              sum[j & 3] += p0 + p1;
-              hi[j] = pack_bf16x2(p0, p1);
-              lo[j] = pack_bf16x2(p0 - __uint_as_float(hi[j] << 16), p1 - __uint_as_float(hi[j] & 0xFFFF0000u));
-            }
-            tc_st16(sa + 16 * k, hi);
-            tc_st16(sa + 64 + 16 * k, lo);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tc_wait_st();
+          neg = -m;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_p[st]);
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          if (!idle) {
+            if (half == 1) {
+              tc_wait_ld();
+              if (nk < KT) mask_tail(x, nk - 64);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+              unsigned w[32];  // hi terms, then lo terms
+#pragma unroll
+              for (int j = 0; j < 16; j++) {
+                const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[k][2 * j]), __uint_as_float(x[k][2 * j + 1])),
+                                            make_float2(c, c), make_float2(neg, neg));
+                const float2 p = make_float2(ex2(y.x), ex2(y.y));
+                sum = __fadd2_rn(sum, p);
+                w[j] = pack_bf16x2(p.x, p.y);
+                const float2 h = unpack_bf16x2(w[j]);
+                const float2 d = __fadd2_rn(p, make_float2(-h.x, -h.y));
+                w[16 + j] = pack_bf16x2(d.x, d.y);
+              }
+              tc_st32(sa + 64 * half + 32 * k, w);
+              if (half == 0) tc_ld32(sa + 64 + 32 * k, x[k]);
+            }
+            tc_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tail.p[st][half]);
+        }
+        l += sum.x + sum.y;
       }
+      li0 += 2u * nt;
       if (!ok) break;
-      if (r < valid) P.W.ml[row] = make_float2(m, l);
-      if (steps == 0) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait(&b_o[st], no & 1u));
-      no++;
+      // records. Two query tiles: each stage its own. One: the two stages'
+      // accumulators merged, every warpgroup one half of the columns
+      const bool merge = !two && nt > 1;
+      float f0 = 1.0f, f1 = 0.0f;
+      if (merge) {
+        tail.ml[st][r] = make_float2(m, l);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float2 a = tail.ml[0][r], b = tail.ml[1][r];
+        m = fmaxf(a.x, b.x);
+        f0 = ex2(a.x - m);
+        f1 = ex2(b.x - m);
+        l = a.y * f0 + b.y * f1;
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // before the next segment's write
+      }
+      const bool has = two || merge || st == 0;  // columns to write
+      const int s0 = two ? st : 0;               // the (first) accumulator
+      if (two || merge || st == 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&tail.o[s0], no[s0] & 1u));
+        if (merge && ok) ok = __all_sync(0xffffffffu, mbar_wait(&tail.o[1], no[1] & 1u));
+      }
+      no[0]++;
+      if (two || merge) no[1]++;
       if (!ok) break;
       tc_fence_after();
-      if (!idle) {
+      const long long row = s.rec + (two ? st * 128 : 0) + r;
+      if (!idle && has) {
+        const int c0 = merge ? st * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
 #pragma unroll 1
-        for (int k = 0; k < D / 32; k++) {
-          unsigned o[32];
-          tc_ld32(oa + 32 * k, o);
+        for (int k = c0; k < c1; k += 16) {
+          unsigned a[16], b[16];
+          tc_ld16(oa + s0 * 128 + k, a);
+          if (merge) tc_ld16(oa + 128 + k, b);
           tc_wait_ld();
-          if (r < valid) {
-            float4* dst = reinterpret_cast<float4*>(P.W.rec + row * D + 32 * k);
+          float o[2][8];
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-              dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                   __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+          for (int j = 0; j < 16; j++)
+            o[j / 8][j % 8] = merge ? __uint_as_float(a[j]) * f0 + __uint_as_float(b[j]) * f1 : __uint_as_float(a[j]);
+          if (r < valid) {
+            st_global_v8(P.W.rec + row * D + k, o[0]);
+            st_global_v8(P.W.rec + row * D + k + 8, o[1]);
           }
         }
+        if (r < valid && (two || st == 0)) P.W.ml[row] = make_float2(m, l);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b_ofree[st]);
+      if (lane == 0) mbar_arrive(&tail.ofree);
     }
   }
-  if (!ok && lane == 0) atomicOr(P.D.err, kDevTimeout);
+  if (!ok && lane == 0 && warp != 9) atomicOr(P.D.err, kDevTimeout);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

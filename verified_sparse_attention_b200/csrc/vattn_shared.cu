@@ -13,7 +13,8 @@ namespace {
 
 struct SharedKernels {
   void (*prefix)(SharedParams);
-  int RB, KT, split;
+  int RB, KT;
+  bool tc;  // the tensor-core prefix kernel
   unsigned threads;
   size_t smem;
   void (*own)(DevParams);   // the gather of the sequences' own positions
@@ -29,7 +30,7 @@ SharedKernels kernels_for(bool host_kv) {
   k.prefix = vattn::k_shared_prefix<T, D>;
   k.RB = vattn::PrefixShape<D>::RB;
   k.KT = vattn::PrefixShape<D>::KT;
-  k.split = 0;
+  k.tc = false;
   k.threads = 256;
   k.smem = vattn::PrefixShape<D>::SMEM;
   k.own = host_kv ? vattn::k_gather<T, D, G, kModeSuffix, true> : vattn::k_gather<T, D, G, kModeSuffix>;
@@ -39,7 +40,7 @@ SharedKernels kernels_for(bool host_kv) {
       k.prefix = vattn::k_shared_prefix_tc<D>;
       k.RB = 2 * vattn::PrefixTcShape<D>::M;
       k.KT = vattn::PrefixTcShape<D>::KT;
-      k.split = 1;
+      k.tc = true;
       k.threads = vattn::PrefixTcShape<D>::THREADS;
       k.smem = vattn::PrefixTcShape<D>::SMEM;
       k.own = vattn::k_gather_tc<D, G, kModeSuffix>;
@@ -102,24 +103,23 @@ size_t shared_workspace(vattn_ctx* ctx, char* p) {
   const vattn_config& c = ctx->cfg;
   const SharedKernels k = pick(ctx);
   const size_t B = static_cast<size_t>(c.max_batch);
-  // one block's rows per CTA for segments that a CTA's end cuts, and every
-  // block's rows once (twice in a block that keeps two records a row)
-  const size_t rows = static_cast<size_t>(ctx->num_sms) * k.RB + (k.split ? 2 : 1) * B * c.num_q_heads;
-  const size_t sz_int = align256(B * sizeof(int)), sz_sum = align256((B + 1) * sizeof(long long));
+  // every block's rows once, and one block's rows per CTA for segments that a
+  // CTA's end cuts
+  const size_t rows = static_cast<size_t>(ctx->num_sms) * k.RB + B * c.num_q_heads;
+  const size_t sz_int = align256(B * sizeof(int)), sz_group = align256((B + 1) * sizeof(SharedGroup));
   const size_t sz_rec = align256(rows * c.head_dim * sizeof(float)), sz_ml = align256(rows * sizeof(float2));
   if (p) {
     SharedWork& w = ctx->shared;
     w.reach = reinterpret_cast<int*>(p); p += sz_int;
     w.pages_ok = reinterpret_cast<int*>(p); p += sz_int;
-    w.tiles = reinterpret_cast<long long*>(p); p += sz_sum;
-    w.rows = reinterpret_cast<long long*>(p); p += sz_sum;
+    w.group = reinterpret_cast<SharedGroup*>(p); p += sz_group;
     w.rec = reinterpret_cast<float*>(p); p += sz_rec;
     w.ml = reinterpret_cast<float2*>(p);
     w.grid = ctx->num_sms;
     cudaFuncSetAttribute(k.prefix, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
     cudaFuncSetAttribute(k.own, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.own_smem));
   }
-  return 2 * sz_int + 2 * sz_sum + sz_rec + sz_ml;
+  return 2 * sz_int + sz_group + sz_rec + sz_ml;
 }
 
 }  // namespace vattn
@@ -163,8 +163,7 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
   P.groups = groups;
   P.RB = k.RB;
   P.KT = k.KT;
-  P.split = k.split;
-  if (k.split)
+  if (k.tc)
     if (const int rc = encode_tile_maps(c, ctx->G, q, k_cache, v_cache, batch, num_pages, &P))
       return ctx->last_status = rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

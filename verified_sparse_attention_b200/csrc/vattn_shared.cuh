@@ -37,36 +37,15 @@ struct SharedParams {
   const int* prefix_lens;
   int groups;
   int RB, KT;  // rows of a block, keys of a tile
-  int split;   // 1: blocks of at most RB / 2 rows keep two records a row
   int box;     // rows of a cache box: a power of two that divides the page size, at most KT
 };
 
 // ---------------------------------------------------------------- groups
-struct Group {
-  int b0, size;  // its sequences
-  int prefix;
-  int tiles;     // key tiles of the prefix (0: not shared)
-};
-__device__ __forceinline__ Group group_of(const SharedParams& P, int g) {
-  Group r;
-  r.b0 = P.group_start[g];
-  r.size = P.group_start[g + 1] - r.b0;
-  r.prefix = P.prefix_lens[g];
-  r.tiles = P.W.reach[g] >= 2 ? (r.prefix + P.KT - 1) / P.KT : 0;
-  return r;
-}
-// Record rows of a block with `rows` query rows.
-__device__ __forceinline__ int block_rows(const SharedParams& P, int rows) {
-  return P.split && rows <= P.RB / 2 ? 2 * rows : rows;
-}
-// Record rows of a whole group per KV head.
-__device__ __forceinline__ long long group_rows(const SharedParams& P, int rows) {
-  const int full = rows / P.RB, rest = rows % P.RB;
-  return static_cast<long long>(full) * P.RB + block_rows(P, rest);
-}
-// First record row of a block and head within its group's.
-__device__ __forceinline__ long long block_row0(const SharedParams& P, int mb, int h, int rec_rows) {
-  return static_cast<long long>(mb) * P.RB * P.D.Hkv + static_cast<long long>(h) * rec_rows;
+// Record rows of a whole group's query rows are its query rows per KV head;
+// a block's records of KV head h start behind those of the blocks and heads
+// before it.
+__device__ __forceinline__ long long block_row0(const SharedParams& P, int mb, int h, int rows) {
+  return static_cast<long long>(mb) * P.RB * P.D.Hkv + static_cast<long long>(h) * rows;
 }
 
 // ============================================================ k_shared_prep
@@ -198,12 +177,17 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
   for (int base = 0; base < P.groups; base += blockDim.x) {
     const int g = base + tid;
     long long t = 0, r = 0;
+    SharedGroup rec = {};
     if (g < P.groups && !bad_bounds) {
       const int reach = *static_cast<volatile int*>(&P.W.reach[g]);
+      rec.b0 = P.group_start[g];
+      rec.size = P.group_start[g + 1] - rec.b0;
+      rec.prefix = P.prefix_lens[g];
       if (reach >= 2) {
-        const int nrow = (P.group_start[g + 1] - P.group_start[g]) * D.G;
-        t = static_cast<long long>((P.prefix_lens[g] + P.KT - 1) / P.KT) * ((nrow + P.RB - 1) / P.RB) * D.Hkv;
-        r = group_rows(P, nrow) * D.Hkv;
+        const int nrow = rec.size * D.G;
+        rec.tiles = (rec.prefix + P.KT - 1) / P.KT;
+        t = static_cast<long long>(rec.tiles) * ((nrow + P.RB - 1) / P.RB) * D.Hkv;
+        r = static_cast<long long>(nrow) * D.Hkv;
       }
     }
     // both sums of 256 groups: tiles < 2^24 / KT * batch rows..., kept in 64 bits by a serial scan of warp 0
@@ -219,16 +203,19 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
       __syncthreads();
     }
     if (g < P.groups) {
-      P.W.tiles[g] = tiles + s_t[tid] - t;
-      P.W.rows[g] = rows + s_r[tid] - r;
+      rec.tile0 = tiles + s_t[tid] - t;
+      rec.row0 = rows + s_r[tid] - r;
+      P.W.group[g] = rec;
     }
     tiles += s_t[kSharedPrepThreads - 1];
     rows += s_r[kSharedPrepThreads - 1];
     __syncthreads();
   }
   if (tid == 0) {
-    P.W.tiles[P.groups] = tiles;
-    P.W.rows[P.groups] = rows;
+    SharedGroup rec = {};
+    rec.tile0 = tiles;
+    rec.row0 = rows;
+    P.W.group[P.groups] = rec;
     s_sum[0] = 0;
   }
   __syncthreads();
@@ -269,39 +256,45 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
 // ---------------------------------------------------------------- segments
 // One CTA's part of a (row block, KV head): key tiles [t0, t1).
 struct Segment {
-  Group g;
+  int b0, prefix;       // the group's first sequence and prefix length
   int gi, mb, h, t0, t1;
   int row0, rows;       // the block's query rows within the group
   long long rec;        // its first record row
   long long next;       // flattened tile behind it
 };
 // The segment that starts at flattened tile x of a CTA with tiles up to `end`;
-// gi: the group searched from.
-__device__ __forceinline__ Segment segment_at(const SharedParams& P, long long x, long long end, int gi) {
-  while (P.W.tiles[gi + 1] <= x) gi++;
+// gi: the group searched from. `group`: the records, in global or shared memory.
+__device__ __forceinline__ Segment segment_at(const SharedParams& P, const SharedGroup* group, long long x,
+                                              long long end, int gi) {
+  while (group[gi + 1].tile0 <= x) gi++;
+  const SharedGroup g = group[gi];
   Segment s;
   s.gi = gi;
-  s.g = group_of(P, gi);
-  const long long y = x - P.W.tiles[gi];
-  const int per = s.g.tiles * P.D.Hkv;
+  s.b0 = g.b0;
+  s.prefix = g.prefix;
+  const long long y = x - g.tile0;
+  const int per = g.tiles * P.D.Hkv;
   s.mb = static_cast<int>(div_nonneg(y, per));
   const int z = static_cast<int>(y - static_cast<long long>(s.mb) * per);
-  s.h = z / s.g.tiles;
-  s.t0 = z - s.h * s.g.tiles;
-  s.t1 = static_cast<int>(min(static_cast<long long>(s.g.tiles), s.t0 + (end - x)));
+  s.h = z / g.tiles;
+  s.t0 = z - s.h * g.tiles;
+  s.t1 = static_cast<int>(min(static_cast<long long>(g.tiles), s.t0 + (end - x)));
   s.next = x + (s.t1 - s.t0);
   s.row0 = s.mb * P.RB;
-  s.rows = min(P.RB, s.g.size * P.D.G - s.row0);
-  s.rec = static_cast<long long>(blockIdx.x) * P.RB + P.W.rows[gi] +
-          block_row0(P, s.mb, s.h, block_rows(P, s.rows));
+  s.rows = min(P.RB, g.size * P.D.G - s.row0);
+  s.rec = static_cast<long long>(blockIdx.x) * P.RB + g.row0 + block_row0(P, s.mb, s.h, s.rows);
   return s;
 }
-// Group of a CTA's first tile (the whole block).
-__device__ __forceinline__ int first_group(const SharedParams& P, long long x, int* s_g) {
-  for (int g = threadIdx.x; g < P.groups; g += blockDim.x)
-    if (P.W.tiles[g] <= x && x < P.W.tiles[g + 1]) *s_g = g;
-  __syncthreads();
-  return *s_g;
+// Group of flattened tile x (every warp by itself).
+__device__ __forceinline__ int group_at(const SharedParams& P, const SharedGroup* group, long long x) {
+  const int lane = threadIdx.x & 31;
+  for (int base = 0; base < P.groups; base += 32) {
+    const int g = base + lane;
+    const unsigned hit =
+        __ballot_sync(0xffffffffu, g < P.groups && group[g].tile0 <= x && x < group[g + 1].tile0);
+    if (hit) return base + __ffs(hit) - 1;
+  }
+  return 0;
 }
 
 // ============================================================ k_shared_prefix
@@ -325,19 +318,16 @@ __global__ void __launch_bounds__(256, 1) k_shared_prefix(const __grid_constant_
   float* s_k = s_q + RB * LD;
   float* s_v = s_k + KT * LD;
   float* s_p = s_v + KT * D;
-  __shared__ int s_g;
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-  if (tid == 0) s_g = 0;
-  __syncthreads();
   grid_dependency_wait();
-  const long long Tt = P.W.tiles[P.groups];
+  const long long Tt = P.W.group[P.groups].tile0;
   long long cur = div_nonneg(Tt * blockIdx.x, gridDim.x);
   const long long end = div_nonneg(Tt * (blockIdx.x + 1), gridDim.x);
-  int gi = cur < end ? first_group(P, cur, &s_g) : 0;
+  int gi = group_at(P, P.W.group, cur);
   const float c = P.D.scale * 1.4426950408889634f;  // scores in log2 units
 
   while (cur < end) {
-    const Segment s = segment_at(P, cur, end, gi);
+    const Segment s = segment_at(P, P.W.group, cur, end, gi);
     gi = s.gi;
     cur = s.next;
     if (!P.W.pages_ok[s.gi]) continue;  // the combine does not read its records
@@ -347,7 +337,7 @@ __global__ void __launch_bounds__(256, 1) k_shared_prefix(const __grid_constant_
       float x[E];
       uint4 raw = make_uint4(0u, 0u, 0u, 0u);
       if (r < s.rows) {
-        const int row = s.row0 + r, b = s.g.b0 + row / P.D.G;
+        const int row = s.row0 + r, b = s.b0 + row / P.D.G;
         raw = *reinterpret_cast<const uint4*>(
             q + (static_cast<size_t>(b) * P.D.Hq + s.h * P.D.G + row % P.D.G) * D + e);
       }
@@ -364,13 +354,13 @@ __global__ void __launch_bounds__(256, 1) k_shared_prefix(const __grid_constant_
       for (int j = 0; j < D / 16; j++) o[i][j] = 0.0f;
     }
     for (int t = s.t0; t < s.t1; t++) {
-      const int k0 = t * KT, nk = min(KT, s.g.prefix - k0);
+      const int k0 = t * KT, nk = min(KT, s.prefix - k0);
       __syncthreads();
       for (int i = tid; i < KT * VPR; i += 256) {
         const int r = i / VPR, e = i % VPR * E;
         uint4 kr = make_uint4(0u, 0u, 0u, 0u), vr = kr;
         if (r < nk) {
-          const size_t off = row_off(P.D, s.g.b0, s.h, k0 + r, D) + e;
+          const size_t off = row_off(P.D, s.b0, s.h, k0 + r, D) + e;
           kr = ld_gather(static_cast<const T*>(P.D.k) + off);
           vr = ld_gather(static_cast<const T*>(P.D.v) + off);
         }
@@ -505,22 +495,19 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
   // records of the prefix
   SliceRecs pre{0, 0, 0, false};
   long long Tp = 0, base = 0;
-  int halves = 1, rows = 0;
   const int C = P.W.grid;
   if (shared) {
-    const Group g = group_of(P, inf.k);
-    Tp = P.W.tiles[P.groups];
+    const SharedGroup g = P.W.group[inf.k];
+    Tp = P.W.group[P.groups].tile0;
     const int row = (b - g.b0) * Q.G + gh, mb = row / P.RB;
-    rows = min(P.RB, g.size * Q.G - mb * P.RB);
-    halves = block_rows(P, rows) / rows;
-    base = P.W.rows[inf.k] + block_row0(P, mb, h, halves * rows) + (row - mb * P.RB);
-    const long long x0 = P.W.tiles[inf.k] + (static_cast<long long>(mb) * Q.Hkv + h) * g.tiles;
-    pre.x0 = x0;
+    const int rows = min(P.RB, g.size * Q.G - mb * P.RB);
+    base = g.row0 + block_row0(P, mb, h, rows) + (row - mb * P.RB);
+    pre.x0 = g.tile0 + (static_cast<long long>(mb) * Q.Hkv + h) * g.tiles;
     pre.per_item = Tp < C;
-    pre.cf = pre.per_item ? 0 : cta_of(x0, Tp, C);
-    pre.n = pre.per_item ? g.tiles : cta_of(x0 + g.tiles - 1, Tp, C) - pre.cf + 1;
+    pre.cf = pre.per_item ? 0 : cta_of(pre.x0, Tp, C);
+    pre.n = pre.per_item ? g.tiles : cta_of(pre.x0 + g.tiles - 1, Tp, C) - pre.cf + 1;
   }
-  const int np = pre.n * halves, N = np + own.n;
+  const int np = pre.n, N = np + own.n;
   float m = -INFINITY, l = 0.0f, a[PL];
 #pragma unroll
   for (int i = 0; i < PL; i++) a[i] = 0.0f;
@@ -528,8 +515,7 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
     float rm, rl;
     const float* src;
     if (j < np) {
-      const long long row = static_cast<long long>(slice_rec(pre, Tp, C, j / halves)) * P.RB + base +
-                            (j % halves) * rows;
+      const long long row = static_cast<long long>(slice_rec(pre, Tp, C, j)) * P.RB + base;
       const float2 v = P.W.ml[row];
       rm = v.x;
       rl = v.y;
