@@ -22,11 +22,16 @@ struct alignas(16) SharedGroup {
 
 // Workspace of the shared-prefix decode (see vattn_shared.cuh).
 struct SharedWork {
-  int* reach = nullptr;           // [max_batch] per group: sequences that reach the prefix's end
+  int* reach = nullptr;           // [2 max_batch] scratch of k_shared_prep's last two CTAs
   int* pages_ok = nullptr;        // [max_batch] per group: the prefix's pages are valid
   SharedGroup* group = nullptr;   // [max_batch + 1]
   float* rec = nullptr;           // [record rows][D]
   float2* ml = nullptr;           // [record rows] (maximum in log2 units, weight sum)
+  int* own_pre = nullptr;         // [max_batch + 1] prefix sum of own pieces (of one KV head) over sequences
+  int* own_next = nullptr;        // [0]: pieces handed out, [1]: chunks of a piece
+  float* own_rec = nullptr;       // [pieces][G][D]
+  float2* own_ml = nullptr;       // [pieces][G]
+  int own_warps = 0;              // warps of k_shared_own (0: not used)
   int grid = 0;                   // CTAs of the prefix kernel
 };
 

@@ -1961,7 +1961,7 @@ __global__ void __launch_bounds__(TcShape<D, G>::NW * 32, 1) k_gather_tc(const _
   using S = TcShape<D, G>;
   constexpr int R = S::R, H = S::H, HALF = S::HALF, MATB = S::MATB, BLKB = S::BLKB, NW = S::NW, NS = S::NS,
                 KT = S::KT, REC = S::REC;
-  static_assert(MODE == kModeSample || MODE == kModeDense || MODE == kModeSuffix, "sample and dense gathers");
+  static_assert(MODE == kModeSample || MODE == kModeDense, "sample and dense gathers");
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -2039,7 +2039,6 @@ __global__ void __launch_bounds__(TcShape<D, G>::NW * 32, 1) k_gather_tc(const _
       const int x = t * R + lane;
       if (t >= nbw || lane >= R || x >= nitems) return -1;
       if (MODE == kModeDense) return lb + x;
-      if (MODE == kModeSuffix) return inf.s1 + lb + x;
       return sel[inf.nI + (whole_tail ? lb + x : inf.p + lb + x)];
     };
     auto pid_of = [&](int pos) -> int {

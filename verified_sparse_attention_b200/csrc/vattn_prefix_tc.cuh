@@ -146,13 +146,6 @@ __host__ __device__ constexpr unsigned tc_idesc(int n, bool b_cols) {
          (static_cast<unsigned>(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
-      : "memory");
-}
 __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
@@ -227,6 +220,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
     tc_fence_before();
   }
   grid_dependency_wait();
+  grid_dependents_launch();  // the next kernel takes each SM as this one leaves it (k_shared_own)
   // the groups' records, all at once
   const bool cached = P.groups <= S::GROUPS;
   if (cached) {
@@ -530,7 +524,6 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  grid_dependents_launch();
   if (warp == 9)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }

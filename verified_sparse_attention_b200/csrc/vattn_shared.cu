@@ -17,10 +17,14 @@ struct SharedKernels {
   bool tc;  // the tensor-core prefix kernel
   unsigned threads;
   size_t smem;
-  void (*own)(DevParams);   // the gather of the sequences' own positions
-  unsigned own_threads;
+  void (*own)(SharedParams);  // the sequences' own positions; nullptr: by the gather
+  int own_nw;                 // its warps per CTA (one CTA per SM)
   size_t own_smem;
-  void (*combine)(SharedParams);
+  void (*gather)(DevParams);
+  unsigned gather_threads;
+  size_t gather_smem;
+  void (*combine)(SharedParams);      // one warp per row
+  void (*combine_few)(SharedParams);  // one CTA per row
 };
 
 template <typename T, int D, int G>
@@ -33,8 +37,10 @@ SharedKernels kernels_for(bool host_kv) {
   k.tc = false;
   k.threads = 256;
   k.smem = vattn::PrefixShape<D>::SMEM;
-  k.own = host_kv ? vattn::k_gather<T, D, G, kModeSuffix, true> : vattn::k_gather<T, D, G, kModeSuffix>;
-  k.own_smem = vattn::GatherShape<T, D, G>::SMEM;
+  k.own = nullptr;
+  k.gather = host_kv ? vattn::k_gather<T, D, G, kModeSuffix, true> : vattn::k_gather<T, D, G, kModeSuffix>;
+  k.gather_smem = vattn::GatherShape<T, D, G>::SMEM;
+  k.gather_threads = vattn::GatherShape<T, D, G>::NW * 32;
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
     if (!host_kv) {
       k.prefix = vattn::k_shared_prefix_tc<D>;
@@ -43,12 +49,13 @@ SharedKernels kernels_for(bool host_kv) {
       k.tc = true;
       k.threads = vattn::PrefixTcShape<D>::THREADS;
       k.smem = vattn::PrefixTcShape<D>::SMEM;
-      k.own = vattn::k_gather_tc<D, G, kModeSuffix>;
-      k.own_smem = vattn::TcShape<D, G>::SMEM;
+      k.own = vattn::k_shared_own<D, G>;
+      k.own_nw = vattn::OwnShape<D>::NW;
+      k.own_smem = vattn::OwnShape<D>::SMEM;
     }
   }
-  k.own_threads = vattn::GatherShape<T, D, G>::NW * 32;
-  k.combine = vattn::k_shared_combine<D>;
+  k.combine = vattn::k_shared_combine<D, 1>;
+  k.combine_few = vattn::k_shared_combine<D, vattn::kSharedCombWarps>;
   return k;
 }
 
@@ -71,12 +78,16 @@ int encode_tile_maps(const vattn_config& c, int G, const void* q, const void* k,
   const cuuint64_t d = static_cast<cuuint64_t>(c.head_dim);
   const cuuint64_t rows = static_cast<cuuint64_t>(num_pages) * c.num_kv_heads * static_cast<cuuint64_t>(c.page_size);
   const cuuint64_t dims[2] = {d, rows}, strides[1] = {2 * d};
-  const cuuint32_t boxes[2] = {64u, static_cast<cuuint32_t>(box)}, one[3] = {1u, 1u, 1u};
-  for (int i = 0; i < 2; i++)
-    if (fn(i ? &P->tmv_t : &P->tmk_t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(i ? v : k), dims, strides,
-           boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return VATTN_ECUDA;
+  const cuuint32_t one[3] = {1u, 1u, 1u};
+  auto cache_map = [&](CUtensorMap* map, const void* p, int r) {
+    const cuuint32_t boxes[2] = {64u, static_cast<cuuint32_t>(r)};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, boxes, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (!cache_map(&P->tmk_t, k, box) || !cache_map(&P->tmv_t, v, box) ||
+      !cache_map(&P->tmk_16, k, vattn::kOwnChunk) || !cache_map(&P->tmv_16, v, vattn::kOwnChunk))
+    return VATTN_ECUDA;
   const cuuint64_t Hq = static_cast<cuuint64_t>(c.num_q_heads);
   const cuuint64_t qd[3] = {d, Hq, static_cast<cuuint64_t>(batch)}, qs[2] = {2 * d, 2 * d * Hq};
   const cuuint32_t qb[3] = {64u, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(128 / G)};
@@ -107,19 +118,31 @@ size_t shared_workspace(vattn_ctx* ctx, char* p) {
   // CTA's end cuts
   const size_t rows = static_cast<size_t>(ctx->num_sms) * k.RB + B * c.num_q_heads;
   const size_t sz_int = align256(B * sizeof(int)), sz_group = align256((B + 1) * sizeof(SharedGroup));
+  const size_t sz_pre = align256((B + 1) * sizeof(int));
   const size_t sz_rec = align256(rows * c.head_dim * sizeof(float)), sz_ml = align256(rows * sizeof(float2));
+  const int own_warps = k.own ? k.own_nw * ctx->num_sms : 0;
+  // at most kOwnPieces pieces per warp, and one more per (sequence, KV head)
+  const size_t own_rows =
+      k.own ? (static_cast<size_t>(vattn::kOwnPieces) * own_warps + B * c.num_kv_heads) * ctx->G : 0;
+  const size_t sz_orec = align256(own_rows * c.head_dim * sizeof(float)), sz_oml = align256(own_rows * sizeof(float2));
   if (p) {
     SharedWork& w = ctx->shared;
-    w.reach = reinterpret_cast<int*>(p); p += sz_int;
+    w.reach = reinterpret_cast<int*>(p); p += 2 * sz_int;
     w.pages_ok = reinterpret_cast<int*>(p); p += sz_int;
     w.group = reinterpret_cast<SharedGroup*>(p); p += sz_group;
     w.rec = reinterpret_cast<float*>(p); p += sz_rec;
-    w.ml = reinterpret_cast<float2*>(p);
+    w.ml = reinterpret_cast<float2*>(p); p += sz_ml;
+    w.own_pre = reinterpret_cast<int*>(p); p += sz_pre;
+    w.own_next = reinterpret_cast<int*>(p); p += 256;
+    w.own_rec = reinterpret_cast<float*>(p); p += sz_orec;
+    w.own_ml = reinterpret_cast<float2*>(p);
+    w.own_warps = own_warps;
     w.grid = ctx->num_sms;
     cudaFuncSetAttribute(k.prefix, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
-    cudaFuncSetAttribute(k.own, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.own_smem));
+    if (k.own) cudaFuncSetAttribute(k.own, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.own_smem));
+    cudaFuncSetAttribute(k.gather, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.gather_smem));
   }
-  return 2 * sz_int + sz_group + sz_rec + sz_ml;
+  return 3 * sz_int + sz_pre + 256 + sz_group + sz_rec + sz_ml + sz_orec + sz_oml;
 }
 
 }  // namespace vattn
@@ -148,8 +171,9 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
   P.D.dense = 1;
   P.D.proxy = VATTN_EXACT;
   if (const int rc = vattn::cache_ptrs(c, &k_cache, &v_cache)) return ctx->last_status = rc;
-  if (!P.D.kv_host)
-    if (const int rc = vattn::encode_row_maps(c, k_cache, v_cache, num_pages, &P.D)) return ctx->last_status = rc;
+  if (static_cast<unsigned long long>(num_pages) * c.num_kv_heads * static_cast<unsigned long long>(c.page_size) >
+      0x7FFFFFFFull)
+    return VATTN_EINVAL;  // row coordinates are 32-bit
   P.D.q = q;
   P.D.k = k_cache;
   P.D.v = v_cache;
@@ -163,14 +187,26 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
   P.groups = groups;
   P.RB = k.RB;
   P.KT = k.KT;
+  P.own_warps = ctx->shared.own_warps;
+  if (!k.own && !P.D.kv_host)
+    if (const int rc = vattn::encode_row_maps(c, k_cache, v_cache, num_pages, &P.D)) return ctx->last_status = rc;
   if (k.tc)
     if (const int rc = encode_tile_maps(c, ctx->G, q, k_cache, v_cache, batch, num_pages, &P))
       return ctx->last_status = rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int launches = 0;
-  vattn::launch(vattn::k_shared_prep, dim3(batch + groups + 1), dim3(vattn::kSharedPrepThreads), 0, st, P, &launches);
+  vattn::launch(vattn::k_shared_prep, dim3(batch + groups + 2), dim3(vattn::kSharedPrepThreads), 0, st, P, &launches);
   vattn::launch(k.prefix, dim3(ctx->num_sms), dim3(k.threads), k.smem, st, P, &launches);
-  vattn::launch(k.own, dim3(ctx->gather_grid), dim3(k.own_threads), k.own_smem, st, P.D, &launches);
-  vattn::launch(k.combine, dim3(P.D.units, ctx->G), dim3(vattn::kSharedCombWarps * 32), 0, st, P, &launches);
+  if (k.own)
+    vattn::launch(k.own, dim3(ctx->num_sms), dim3(k.own_nw * 32), k.own_smem, st, P, &launches);
+  else
+    vattn::launch(k.gather, dim3(ctx->gather_grid), dim3(k.gather_threads), k.gather_smem, st, P.D, &launches);
+  // a CTA per row while these are resident together (eight per SM), else a
+  // warp per row
+  const int rows = batch * c.num_q_heads;
+  const bool few = rows <= 8 * ctx->num_sms;
+  vattn::launch(few ? k.combine_few : k.combine,
+                dim3(few ? rows : (rows + vattn::kSharedCombWarps - 1) / vattn::kSharedCombWarps),
+                dim3(vattn::kSharedCombWarps * 32), 0, st, P, &launches);
   return vattn::finish(ctx, launches);
 }

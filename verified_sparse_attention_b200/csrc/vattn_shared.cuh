@@ -1,10 +1,11 @@
 // Kernels of the shared-prefix decode (vattn_shared_dense_decode), in launch
 // order:
 //
-//   k_shared_prep     validates lengths, groups and pages; the work of the
-//                     prefix kernel and of the gather as prefix sums
+//   k_shared_prep     validates lengths, groups and pages; the work of the two
+//                     kernels behind it as prefix sums
 //   k_shared_prefix(_tc)  every group's prefix against all of its queries
-//   k_gather(_tc)<kModeSuffix>  every sequence's own positions
+//   k_shared_own      every sequence's own positions (bf16 caches in device
+//                     memory; others: k_gather<kModeSuffix>)
 //   k_shared_combine  merges the records of both parts
 //
 // A group's G * (its sequences) query rows of one KV head meet the same keys,
@@ -14,7 +15,7 @@
 // head) segment leaves one record (maximum, weight sum, weighted values) per
 // row. Only groups of which two sequences at least reach the end of the prefix
 // are shared: the others, and sequences shorter than their prefix, are left to
-// the gather whole, so that no row of a segment is masked and every key of a
+// the own part whole, so that no row of a segment is masked and every key of a
 // tile counts for every row.
 #pragma once
 
@@ -31,6 +32,7 @@ struct SharedParams {
   // the queries [batch][Hq][d] in boxes of 128 rows (128 / G sequences, the G
   // heads of a KV head) by 64 columns, 128-byte swizzle
   CUtensorMap tmk_t, tmv_t, tmq;
+  CUtensorMap tmk_16, tmv_16;  // the caches in boxes of 16 rows (k_shared_own)
   DevParams D;
   SharedWork W;
   const int* group_start;
@@ -38,6 +40,7 @@ struct SharedParams {
   int groups;
   int RB, KT;  // rows of a block, keys of a tile
   int box;     // rows of a cache box: a power of two that divides the page size, at most KT
+  int own_warps;  // k_shared_own's warps; 0: the gather takes the own positions
 };
 
 // ---------------------------------------------------------------- groups
@@ -48,8 +51,19 @@ __device__ __forceinline__ long long block_row0(const SharedParams& P, int mb, i
   return static_cast<long long>(mb) * P.RB * P.D.Hkv + static_cast<long long>(h) * rows;
 }
 
+// Chunks of k_shared_own that cover positions [start, n): kOwnChunk positions
+// each from the 16-position block that holds `start`. Warps take them in pieces
+// of at least kOwnPiece chunks of one (sequence, KV head), about kOwnPieces a
+// warp when there are many.
+constexpr int kOwnPiece = 8, kOwnPieces = 4;
+constexpr int kOwnChunk = 16;
+__device__ __forceinline__ int own_chunks(int start, int n) {
+  return n > start ? (n - (start & ~15) + kOwnChunk - 1) / kOwnChunk : 0;
+}
+
 // ============================================================ k_shared_prep
 constexpr int kSharedPrepThreads = 256;
+constexpr int kSharedPrepKeep = 1024;  // sequences and groups kept in shared memory by the last CTA
 
 __device__ __forceinline__ int checked_len(const SharedParams& P, int b) {
   const int n = P.D.seq_lens[b];
@@ -83,69 +97,81 @@ __device__ __forceinline__ int count_reach(const SharedParams& P, int b0, int b1
   return cnt;
 }
 
-// CTA b < batch: sequence b; CTA batch + g: group g (its pages and count); the
-// last CTA: the prefix sums.
+// Inclusive 64-bit prefix sum over the block's 256 threads.
+__device__ __forceinline__ long long block_scan_ll(long long v, long long* s_w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  if (lane == 31) s_w[warp] = v;  // the warps' sums stay there
+  __syncthreads();
+  for (int w = 0; w < warp; w++) v += s_w[w];
+  __syncthreads();
+  return v;
+}
+
+// CTA b < batch: sequence b; CTA batch + g: group g (its pages); the last two
+// CTAs: the prefix kernel's work and the own parts' as prefix sums.
 static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const __grid_constant__ SharedParams P) {
-  __shared__ unsigned s_warp[32];
-  __shared__ int s_g, s_bad;
   const int tid = threadIdx.x, cta = blockIdx.x;
   const DevParams& D = P.D;
-  if (tid == 0) {
-    s_g = -1;
-    s_bad = 0;
-  }
+  grid_dependents_launch();
   grid_dependency_wait();
-  __syncthreads();
-  // the bounds ascend from 0 to batch, or nothing is decoded; with ascending
-  // bounds at most one group holds a sequence
-  for (int g = tid; g < P.groups; g += blockDim.x) {
-    const int lo = P.group_start[g], hi = P.group_start[g + 1];
-    if (hi < lo || (g == 0 && lo != 0) || (g == P.groups - 1 && hi != D.batch)) s_bad = 1;
-    if (cta < D.batch && lo <= cta && cta < hi) s_g = g;
-  }
-  __syncthreads();
-  const bool bad_bounds = s_bad != 0;
 
-  if (cta < D.batch) {
-    const int b = cta, g = s_g;
-    int n = checked_len(P, b), start = 0;
-    if (tid == 0 && n < 0) atomicOr(D.err, kDevBadSeqlen);
-    if (n < 0 || bad_bounds || g < 0) n = 0;
-    if (n > 0) {
-      const int prefix = P.prefix_lens[g];
-      if (prefix < 0 || prefix > D.max_ctx) {
-        n = 0;
-      } else if (n >= prefix && prefix > 0) {
-        if (count_reach(P, P.group_start[g], P.group_start[g + 1], prefix) >= 2) start = prefix;
-      }
+  if (cta < D.batch + P.groups) {
+    __shared__ int s_g, s_bad;
+    if (tid == 0) {
+      s_g = -1;
+      s_bad = 0;
     }
-    if (bad_pages(P, b, start / D.ps, (n + D.ps - 1) / D.ps)) {
+    __syncthreads();
+    // the bounds ascend from 0 to batch, or nothing is decoded; with ascending
+    // bounds at most one group holds a sequence
+    for (int g = tid; g < P.groups; g += blockDim.x) {
+      const int lo = P.group_start[g], hi = P.group_start[g + 1];
+      if (hi < lo || (g == 0 && lo != 0) || (g == P.groups - 1 && hi != D.batch)) s_bad = 1;
+      if (cta < D.batch && lo <= cta && cta < hi) s_g = g;
+    }
+    __syncthreads();
+    const bool bad_bounds = s_bad != 0;
+    if (cta < D.batch) {
+      const int b = cta, g = s_g;
+      int n = checked_len(P, b), start = 0;
+      if (tid == 0 && n < 0) atomicOr(D.err, kDevBadSeqlen);
+      if (n < 0 || bad_bounds || g < 0) n = 0;
+      if (n > 0) {
+        const int prefix = P.prefix_lens[g];
+        if (prefix < 0 || prefix > D.max_ctx) {
+          n = 0;
+        } else if (n >= prefix && prefix > 0) {
+          if (count_reach(P, P.group_start[g], P.group_start[g + 1], prefix) >= 2) start = prefix;
+        }
+      }
       // only the positions behind the prefix are read through this row
-      if (n > start) {
+      if (n > start && bad_pages(P, b, start / D.ps, (n + D.ps - 1) / D.ps)) {
         if (tid == 0) atomicOr(D.err, kDevBadPage);
         n = 0;
       }
+      for (int h = tid; h < D.Hkv; h += blockDim.x) {
+        UnitInfo inf = {};
+        inf.n = n;
+        inf.s1 = start;
+        inf.k = g;
+        D.info[static_cast<size_t>(b) * D.Hkv + h] = inf;
+      }
+      return;
     }
-    for (int h = tid; h < D.Hkv; h += blockDim.x) {
-      UnitInfo inf = {};
-      inf.n = n;
-      inf.s1 = start;
-      inf.k = g;
-      D.info[static_cast<size_t>(b) * D.Hkv + h] = inf;
-    }
-    return;
-  }
-  if (cta < D.batch + P.groups) {
     const int g = cta - D.batch;
-    int reach = 0, ok = 0;
+    int ok = 0;
     if (!bad_bounds) {
       const int prefix = P.prefix_lens[g], b0 = P.group_start[g], b1 = P.group_start[g + 1];
       if (prefix < 0 || prefix > D.max_ctx) {
         if (tid == 0) atomicOr(D.err, kDevBadGroup);
       } else {
-        reach = count_reach(P, b0, b1, prefix);
         ok = 1;
-        if (reach >= 2 && bad_pages(P, b0, 0, (prefix + D.ps - 1) / D.ps)) {
+        if (count_reach(P, b0, b1, prefix) >= 2 && bad_pages(P, b0, 0, (prefix + D.ps - 1) / D.ps)) {
           if (tid == 0) atomicOr(D.err, kDevBadPage);
           ok = 0;
         }
@@ -154,92 +180,144 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
     if (tid == 0) P.W.pages_ok[g] = ok;
     return;
   }
-  // prefix sums: key tiles and record rows over groups, the gather's slices
-  if (bad_bounds && tid == 0) atomicOr(D.err, kDevBadGroup);
-  for (int g = tid; g < P.groups; g += blockDim.x) P.W.reach[g] = 0;
+
+  // ---- prefix sums. The inputs come into shared memory in one round of loads
+  // (what does not fit is read where it is).
+  const bool own_cta = cta == D.batch + P.groups + 1;
+  int* g_reach = P.W.reach + (own_cta ? P.groups : 0);
+  __shared__ int s_len[kSharedPrepKeep], s_prefix[kSharedPrepKeep], s_reach[kSharedPrepKeep];
+  __shared__ int s_start[kSharedPrepKeep + 1];
+  __shared__ long long s_w[kSharedPrepThreads / 32], s_carry[2];
+  __shared__ int s_bad;
+  for (int b = tid; b < min(D.batch, kSharedPrepKeep); b += blockDim.x) s_len[b] = checked_len(P, b);
+  for (int g = tid; g < min(P.groups, kSharedPrepKeep); g += blockDim.x) {
+    s_prefix[g] = P.prefix_lens[g];
+    s_reach[g] = 0;
+  }
+  for (int g = tid; g < min(P.groups, kSharedPrepKeep) + 1; g += blockDim.x) s_start[g] = P.group_start[g];
+  for (int g = kSharedPrepKeep + tid; g < P.groups; g += blockDim.x) g_reach[g] = 0;
+  if (tid == 0) {
+    s_bad = 0;
+    s_carry[0] = s_carry[1] = 0;
+  }
   __syncthreads();
+  auto len = [&](int b) -> int { return b < kSharedPrepKeep ? s_len[b] : checked_len(P, b); };
+  auto start_of = [&](int g) -> int { return g <= kSharedPrepKeep ? s_start[g] : P.group_start[g]; };
+  auto prefix_of = [&](int g) -> int { return g < kSharedPrepKeep ? s_prefix[g] : P.prefix_lens[g]; };
+  auto reach_of = [&](int g) -> int {
+    return g < kSharedPrepKeep ? s_reach[g] : *static_cast<volatile int*>(&g_reach[g]);
+  };
+  auto group_of = [&](int b) -> int {  // the last g with group_start[g] <= b
+    int lo = 0, hi = P.groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (start_of(mid) <= b) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
+  for (int g = tid; g < P.groups; g += blockDim.x) {
+    const int lo = start_of(g), hi = start_of(g + 1);
+    if (hi < lo || (g == 0 && lo != 0) || (g == P.groups - 1 && hi != D.batch)) s_bad = 1;
+  }
+  __syncthreads();
+  const bool bad_bounds = s_bad != 0;
+  if (bad_bounds && tid == 0 && !own_cta) atomicOr(D.err, kDevBadGroup);
   if (!bad_bounds) {
     for (int b = tid; b < D.batch; b += blockDim.x) {
-      int lo = 0, hi = P.groups;  // the last g with group_start[g] <= b
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (P.group_start[mid] <= b) lo = mid;
-        else hi = mid;
-      }
-      const int prefix = P.prefix_lens[lo];
-      if (prefix > 0 && prefix <= D.max_ctx && checked_len(P, b) >= prefix) atomicAdd(&P.W.reach[lo], 1);
+      const int g = group_of(b), prefix = prefix_of(g);
+      if (prefix > 0 && prefix <= D.max_ctx && len(b) >= prefix)
+        atomicAdd(g < kSharedPrepKeep ? &s_reach[g] : &g_reach[g], 1);
     }
   }
   __threadfence_block();
   __syncthreads();
-  __shared__ long long s_sum[2];
-  long long tiles = 0, rows = 0;
-  for (int base = 0; base < P.groups; base += blockDim.x) {
-    const int g = base + tid;
-    long long t = 0, r = 0;
-    SharedGroup rec = {};
-    if (g < P.groups && !bad_bounds) {
-      const int reach = *static_cast<volatile int*>(&P.W.reach[g]);
-      rec.b0 = P.group_start[g];
-      rec.size = P.group_start[g + 1] - rec.b0;
-      rec.prefix = P.prefix_lens[g];
-      if (reach >= 2) {
-        const int nrow = rec.size * D.G;
-        rec.tiles = (rec.prefix + P.KT - 1) / P.KT;
-        t = static_cast<long long>(rec.tiles) * ((nrow + P.RB - 1) / P.RB) * D.Hkv;
-        r = static_cast<long long>(nrow) * D.Hkv;
+  if (!own_cta) {
+    // key tiles and record rows over groups
+    long long tiles = 0, rows = 0;
+    for (int base = 0; base < P.groups; base += blockDim.x) {
+      const int g = base + tid;
+      long long t = 0, r = 0;
+      SharedGroup rec = {};
+      if (g < P.groups && !bad_bounds) {
+        rec.b0 = start_of(g);
+        rec.size = start_of(g + 1) - rec.b0;
+        rec.prefix = prefix_of(g);
+        if (reach_of(g) >= 2) {
+          const int nrow = rec.size * D.G;
+          rec.tiles = (rec.prefix + P.KT - 1) / P.KT;
+          t = static_cast<long long>(rec.tiles) * ((nrow + P.RB - 1) / P.RB) * D.Hkv;
+          r = static_cast<long long>(nrow) * D.Hkv;
+        }
       }
-    }
-    // both sums of 256 groups: tiles < 2^24 / KT * batch rows..., kept in 64 bits by a serial scan of warp 0
-    __shared__ long long s_t[kSharedPrepThreads], s_r[kSharedPrepThreads];
-    s_t[tid] = t;
-    s_r[tid] = r;
-    __syncthreads();
-    for (int o = 1; o < kSharedPrepThreads; o <<= 1) {
-      const long long a = tid >= o ? s_t[tid - o] : 0, c = tid >= o ? s_r[tid - o] : 0;
+      const long long it = block_scan_ll(t, s_w), ir = block_scan_ll(r, s_w);
+      if (g < P.groups) {
+        rec.tile0 = tiles + it - t;
+        rec.row0 = rows + ir - r;
+        P.W.group[g] = rec;
+      }
+      if (tid == blockDim.x - 1) {
+        s_carry[0] += it;
+        s_carry[1] += ir;
+      }
       __syncthreads();
-      s_t[tid] += a;
-      s_r[tid] += c;
+      tiles = s_carry[0];
+      rows = s_carry[1];
       __syncthreads();
     }
-    if (g < P.groups) {
-      rec.tile0 = tiles + s_t[tid] - t;
-      rec.row0 = rows + s_r[tid] - r;
-      P.W.group[g] = rec;
+    if (tid == 0) {
+      SharedGroup rec = {};
+      rec.tile0 = tiles;
+      rec.row0 = rows;
+      P.W.group[P.groups] = rec;
     }
-    tiles += s_t[kSharedPrepThreads - 1];
-    rows += s_r[kSharedPrepThreads - 1];
+    return;
+  }
+  // the own parts: a sequence whose pages fail keeps its part here and is
+  // skipped by its kernel
+  auto own_start = [&](int b) -> int {  // -1: no own part
+    if (b >= D.batch || bad_bounds) return -1;
+    const int g = group_of(b), n = len(b), prefix = prefix_of(g);
+    if (n <= 0 || prefix < 0 || prefix > D.max_ctx) return -1;
+    return prefix > 0 && n >= prefix && reach_of(g) >= 2 ? prefix : 0;
+  };
+  if (P.own_warps) {
+    long long sum = 0;  // chunks of one KV head
+    for (int b = tid; b < D.batch; b += blockDim.x) {
+      const int start = own_start(b);
+      if (start >= 0) sum += own_chunks(start, len(b));
+    }
+    block_scan_ll(sum, s_w);
+    if (tid < 32) {
+      long long v = tid < kSharedPrepThreads / 32 ? s_w[tid] : 0;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (tid == 0) s_carry[1] = v;
+    }
     __syncthreads();
+    const long long most = static_cast<long long>(kOwnPieces) * P.own_warps;
+    const int piece = static_cast<int>(max(static_cast<long long>(kOwnPiece), (s_carry[1] * D.Hkv + most - 1) / most));
+    for (int base = 0; base < D.batch; base += blockDim.x) {
+      const int b = base + tid, start = own_start(b);
+      const int cnt = start >= 0 ? (own_chunks(start, len(b)) + piece - 1) / piece : 0;
+      const long long carry = s_carry[0], incl = block_scan_ll(cnt, s_w);
+      if (b < D.batch) P.W.own_pre[b] = static_cast<int>(carry + incl - cnt);
+      __syncthreads();
+      if (tid == blockDim.x - 1) s_carry[0] = carry + incl;
+      __syncthreads();
+    }
+    if (tid == 0) {
+      P.W.own_pre[D.batch] = static_cast<int>(s_carry[0]);
+      P.W.own_next[0] = 0;
+      P.W.own_next[1] = piece;
+    }
+    return;
   }
-  if (tid == 0) {
-    SharedGroup rec = {};
-    rec.tile0 = tiles;
-    rec.row0 = rows;
-    P.W.group[P.groups] = rec;
-    s_sum[0] = 0;
-  }
-  __syncthreads();
-  // slices of the gather: sequence b's own positions, once per KV head (a
-  // sequence whose pages fail keeps its items here and is skipped there)
   for (int base = 0; base < D.batch; base += blockDim.x) {
-    const int b = base + tid;
-    unsigned cnt = 0;
-    if (b < D.batch && !bad_bounds) {
-      int lo = 0, hi = P.groups;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (P.group_start[mid] <= b) lo = mid;
-        else hi = mid;
-      }
-      const int n = checked_len(P, b), prefix = P.prefix_lens[lo];
-      const bool shared = prefix > 0 && prefix <= D.max_ctx && n >= prefix &&
-                          *static_cast<volatile int*>(&P.W.reach[lo]) >= 2;
-      if (n > 0 && prefix >= 0 && prefix <= D.max_ctx) cnt = static_cast<unsigned>(shared ? n - prefix : n);
-    }
-    const long long carry = s_sum[0];
-    const unsigned incl = block_inclusive_scan(cnt, s_warp);  // 256 x 2^24 fits 32 bits unsigned
+    const int b = base + tid, start = own_start(b), cnt = start >= 0 ? len(b) - start : 0;
+    const long long carry = s_carry[0], incl = block_scan_ll(cnt, s_w);
     if (b < D.batch) {
-      const long long at = (carry + (incl - cnt)) * D.Hkv;
+      const long long at = (carry + incl - cnt) * D.Hkv;
       for (int h = 0; h < D.Hkv; h++) {
         const size_t s = 2 * (static_cast<size_t>(b) * D.Hkv + h);
         D.pre_det[s] = at + static_cast<long long>(h) * cnt;
@@ -247,10 +325,10 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
       }
     }
     __syncthreads();
-    if (tid == blockDim.x - 1) s_sum[0] = carry + incl;
+    if (tid == blockDim.x - 1) s_carry[0] = carry + incl;
     __syncthreads();
   }
-  if (tid == 0) D.pre_det[2 * static_cast<size_t>(D.units)] = s_sum[0] * D.Hkv;
+  if (tid == 0) D.pre_det[2 * static_cast<size_t>(D.units)] = s_carry[0] * D.Hkv;
 }
 
 // ---------------------------------------------------------------- segments
@@ -467,31 +545,331 @@ __global__ void __launch_bounds__(256, 1) k_shared_prefix(const __grid_constant_
   grid_dependents_launch();
 }
 
-// ============================================================ k_shared_combine
-// One CTA per (sequence, KV head, query head of the group): folds the records
-// of the prefix segments and of the gather.
-constexpr int kSharedCombWarps = 4;
-
+// ============================================================ k_shared_own
+// Every sequence's positions behind its shared prefix (all of them where
+// nothing is shared), for bf16 caches in device memory. They come in many short
+// runs, so a warp's chunks (16 positions inside one page: 4 KB of K and of V in
+// a row at d = 128) form one stream: a ring of NS chunks in shared memory is
+// filled NS - 1 chunks ahead of the one being computed, across the ends of
+// runs, by two or four tensor copies a chunk. SMs stream at rates that differ
+// by a third, and the prefix kernel leaves them at different times, so warps
+// take pieces of runs from a counter (the first by their index); a piece has
+// the record of its index. The arithmetic of a chunk is k_gather_tc's: S = K q
+// as m16n8k16 products, the online softmax in the accumulator layout,
+// O^T += V^T P with the weights as two bf16 terms.
+// The kernel needs k_shared_prep's results alone: it starts while the prefix
+// kernel's last CTAs run (which start after k_shared_prep's end) and waits
+// for them only before it ends, so that its own end means both. What
+// k_shared_prep wrote is therefore read past L1.
 template <int D>
+struct OwnShape {
+  static constexpr int H = D / 64, KT = D / 16;
+  static constexpr int HALF = 16 * 128;              // 16 rows of a 64-column half
+  static constexpr int MAT = H * HALF;
+  static constexpr int STAGE = 2 * MAT;              // a chunk: K, then V
+  static constexpr int NW = 7, THREADS = NW * 32;
+  static constexpr int NS = D == 128 ? 4 : 6;
+  static constexpr int QUEUE = 8;                    // pieces between the copies and the arithmetic: at most NS + 1
+  static constexpr size_t RING = static_cast<size_t>(NW) * NS * STAGE;
+  static constexpr size_t SMEM = RING + static_cast<size_t>(NW) * (NS * 8 + QUEUE * 24);
+  static_assert(NS + 1 <= QUEUE && SMEM <= 227 * 1024, "shared memory of the own part");
+};
+
+__device__ __forceinline__ UnitInfo load_info(const UnitInfo* p) {
+  UnitInfo inf;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(UnitInfo) / 16); i++)
+    reinterpret_cast<int4*>(&inf)[i] = __ldcg(reinterpret_cast<const int4*>(p) + i);
+  return inf;
+}
+
+// A piece of a run: `chunks` chunks from position `pos` of unit u, whose own
+// positions are [start, n).
+struct OwnPiece {
+  int id, u, pos, chunks, start, n;
+};
+__device__ __forceinline__ OwnPiece own_piece(const SharedParams& P, int id, int per) {
+  const DevParams& Q = P.D;
+  const int lane = threadIdx.x & 31;
+  // the last sequence whose pieces begin at or before id, 32 probes at a time
+  int lo = 0, hi = Q.batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, i < hi && __ldcg(&P.W.own_pre[i]) * Q.Hkv <= id);
+    lo += (__popc(le) - 1) * step;
+    hi = min(lo + step, hi);
+  }
+  const int p0 = __ldcg(&P.W.own_pre[lo]), cnt = __ldcg(&P.W.own_pre[lo + 1]) - p0;
+  const UnitInfo inf = load_info(Q.info + static_cast<size_t>(lo) * Q.Hkv);
+  const int y = id - p0 * Q.Hkv, h = y / cnt, first = (y - h * cnt) * per;
+  OwnPiece r;
+  r.id = id;
+  r.u = lo * Q.Hkv + h;
+  r.pos = (inf.s1 & ~15) + kOwnChunk * first;
+  r.chunks = max(min(per, own_chunks(inf.s1, inf.n) - first), 0);  // none of a sequence that failed
+  r.start = inf.s1;
+  r.n = inf.n;
+  return r;
+}
+
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __grid_constant__ SharedParams P) {
+  using S = OwnShape<D>;
+  constexpr int H = S::H, KT = S::KT, HALF = S::HALF, NS = S::NS, STAGE = S::STAGE, MAT = S::MAT;
+  extern __shared__ __align__(1024) unsigned char s_tiles[];
+  const DevParams& Q = P.D;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = P.own_warps, gw = blockIdx.x * S::NW + warp;
+  unsigned char* ring = s_tiles + warp * NS * STAGE;
+  const unsigned ring_s = smem_u32(ring);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_tiles + S::RING) + warp * NS;
+  OwnPiece* queue = reinterpret_cast<OwnPiece*>(s_tiles + S::RING + S::NW * NS * 8) + warp * S::QUEUE;
+  if (lane < NS) mbar_init(&bars[lane], 1);
+  mbar_init_fence();
+  __syncwarp();
+  const int total = __ldcg(&P.W.own_pre[Q.batch]) * Q.Hkv, per = __ldcg(&P.W.own_next[1]);
+  const float c = Q.scale * 1.4426950408889634f;  // scores in log2 units
+
+  if (gw < total) {
+    // producer: the piece being copied, its next chunk and that chunk's page;
+    // the piece after it
+    OwnPiece pp = own_piece(P, gw, per), pn = pp;
+    bool more = true;         // pn is a piece still to come
+    int px = 0;
+    unsigned nq = 0, dq = 0;  // pieces queued and taken
+    unsigned ni = 0, nc = 0;  // chunks copied and computed (stage and phase follow)
+    auto page_of = [&](const OwnPiece& p, int x) -> int {
+      const int pos = p.pos + kOwnChunk * x;
+      return __ldcg(Q.page_table + static_cast<size_t>(p.u / Q.Hkv) * Q.pps + page_slot(Q, pos));
+    };
+    auto fetch = [&]() {
+      int id = 0;
+      if (lane == 0) id = W + atomicAdd(&P.W.own_next[0], 1);
+      id = __shfl_sync(0xffffffffu, id, 0);
+      more = id < total;
+      if (more) pn = own_piece(P, id, per);
+    };
+    auto enqueue = [&]() {
+      if (pp.chunks == 0) return;
+      if (lane == 0) queue[nq % S::QUEUE] = pp;
+      __syncwarp();
+      nq++;
+    };
+    int page = pp.chunks > 0 ? page_of(pp, 0) : 0, page_n = 0;
+    auto fetch_page = [&]() { page_n = more && pn.chunks > 0 ? page_of(pn, 0) : 0; };
+    enqueue();
+    fetch();
+    fetch_page();
+    auto issue = [&]() {  // one chunk, if there is one and a stage is free
+      if (ni - nc >= NS) return;
+      while (px >= pp.chunks) {
+        if (!more) return;
+        pp = pn;
+        px = 0;
+        page = page_n;
+        enqueue();
+        fetch();
+        fetch_page();
+      }
+      const int pos = pp.pos + kOwnChunk * px;
+      const int row = (page * Q.Hkv + pp.u % Q.Hkv) * Q.ps + (pos - page_slot(Q, pos) * Q.ps);
+      const int st = static_cast<int>(ni % NS);
+      fence_proxy_async();  // the stage's earlier reads come before the copy's writes
+      if (lane == 0) mbar_arrive_expect_tx(&bars[st], STAGE);
+      __syncwarp();
+      if (lane < 2 * H)
+        tma_2d(ring + st * STAGE + lane * HALF, lane < H ? &P.tmk_16 : &P.tmv_16, (lane % H) * 64, row, &bars[st]);
+      ni++;
+      px++;
+      if (px < pp.chunks) page = page_of(pp, px);
+    };
+#pragma unroll 1
+    for (int i = 0; i < NS - 1; i++) issue();
+
+    const int fj = lane >> 3, fr = lane & 7;  // ldmatrix.x4: matrix lane / 8, row lane % 8
+    const int hc = 2 * (lane & 3), ra = lane >> 2;
+    bool ok = true;
+    while (dq < nq && ok) {
+      const OwnPiece cu = queue[dq % S::QUEUE];
+      dq++;
+      // the query operand: lane holds head lane / 4, dims 16 kt + 2 (lane % 4)
+      // + {0, 1} and those + 8 (zero columns past G)
+      unsigned qf[KT][2];
+      {
+        const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(Q.q) +
+                                  (static_cast<size_t>(cu.u / Q.Hkv) * Q.Hq + (cu.u % Q.Hkv) * G + (ra < G ? ra : 0)) * D +
+                                  hc;
+#pragma unroll
+        for (int kt = 0; kt < KT; kt++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const unsigned v = __ldcg(reinterpret_cast<const unsigned*>(qp + 16 * kt + 8 * e));
+            qf[kt][e] = ra < G ? v : 0u;
+          }
+      }
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[KT][4];
+#pragma unroll
+      for (int mt = 0; mt < KT; mt++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[mt][e] = 0.0f;
+#pragma unroll 1
+      for (int x = 0; x < cu.chunks; x++) {
+        issue();  // into the stage that the chunk before left
+        const int st = static_cast<int>(nc % NS);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars[st], (nc / NS) & 1u));
+        if (!ok) break;
+        nc++;
+        const int pos = cu.pos + kOwnChunk * x;
+        const int r0 = max(cu.start - pos, 0), r1 = min(cu.n - pos, 16);  // own rows of the block
+        const unsigned kb = ring_s + st * STAGE, vb = kb + MAT;
+        const bool part = r1 - r0 < 16;
+        if (part) {
+          // V rows of no own key: zeros, whatever the cache holds there
+          for (int i = lane; i < 16 * 8; i += 32)
+            if (i / 8 < r0 || i / 8 >= r1)
+#pragma unroll
+              for (int hf = 0; hf < H; hf++)
+                *reinterpret_cast<uint4*>(ring + st * STAGE + MAT + hf * HALF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          __syncwarp();
+        }
+        // two chains of products: even and odd k-steps
+        float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kt = 0; kt < KT; kt += 2) {
+          unsigned a[4], b[4];
+          ldsm_x4(kb + tc_off(((fj & 1) << 3) | fr, 2 * kt + (fj >> 1)), a);
+          ldsm_x4(kb + tc_off(((fj & 1) << 3) | fr, 2 * kt + 2 + (fj >> 1)), b);
+          mma_bf16(sc, a, qf[kt][0], qf[kt][1]);
+          mma_bf16(sd, b, qf[kt + 1][0], qf[kt + 1][1]);
+        }
+        // online softmax: rows lane / 4 (values 0, 1) and lane / 4 + 8 (2, 3)
+        float sv[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) sv[e] = (sc[e] + sd[e]) * c;
+        if (part) {
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const int r = ra + (e >> 1) * 8;
+            if (r < r0 || r >= r1) sv[e] = -INFINITY;
+          }
+        }
+        float bm[2] = {fmaxf(sv[0], sv[2]), fmaxf(sv[1], sv[3])};
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+          for (int k = 0; k < 2; k++) bm[k] = fmaxf(bm[k], __shfl_xor_sync(0xffffffffu, bm[k], off));
+        if (__any_sync(0xffffffffu, bm[0] > m[0] || bm[1] > m[1])) {
+          float f[2];
+#pragma unroll
+          for (int k = 0; k < 2; k++) {
+            const float nm = fmaxf(fmaxf(m[k], bm[k]), -1e30f);  // finite: scores of -inf weigh exactly 0
+            f[k] = exp2f(m[k] - nm);
+            m[k] = nm;
+            l[k] *= f[k];
+          }
+#pragma unroll
+          for (int mt = 0; mt < KT; mt++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[mt][e] *= f[e & 1];
+        }
+        float pv[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) pv[e] = exp2f(sv[e] - m[e & 1]);
+#pragma unroll
+        for (int k = 0; k < 2; k++) l[k] += pv[k] + pv[2 + k];
+        // the weights as the B operand: transposes of the [row][head pair] fragments
+        unsigned ph0, pl0, ph1, pl1;
+        split_bf16x2(pv[0], pv[1], ph0, pl0);
+        split_bf16x2(pv[2], pv[3], ph1, pl1);
+        ph0 = movm_t(ph0);
+        pl0 = movm_t(pl0);
+        ph1 = movm_t(ph1);
+        pl1 = movm_t(pl1);
+#pragma unroll
+        for (int mt = 0; mt < KT; mt++) {
+          unsigned a[4];
+          ldsm_x4_t(vb + tc_off(((fj >> 1) << 3) | fr, 2 * mt + (fj & 1)), a);
+          mma_bf16(o[mt], a, ph0, ph1);
+          mma_bf16(o[mt], a, pl0, pl1);
+        }
+        __syncwarp();  // the stage is free again
+      }
+      if (!ok) break;
+      // the piece's record: lane holds dims 16 mt + lane / 4 (+ 8)
+      // of heads hc, hc + 1
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+        for (int k = 0; k < 2; k++) l[k] += __shfl_xor_sync(0xffffffffu, l[k], off);
+      const size_t rec = static_cast<size_t>(cu.id) * G;
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        if (hc + k >= G) continue;
+        if (ra == 0) P.W.own_ml[rec + hc + k] = make_float2(m[k], l[k]);
+        float* r = P.W.own_rec + (rec + hc + k) * D + ra;
+#pragma unroll
+        for (int mt = 0; mt < KT; mt++) {
+          r[16 * mt] = o[mt][k];
+          r[16 * mt + 8] = o[mt][2 + k];
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(Q.err, kDevTimeout);
+      for (; nc != ni; nc++) mbar_wait(&bars[nc % NS], (nc / NS) & 1u);  // no copy lands after the warp has moved on
+    }
+  }
+  grid_dependents_launch();
+  grid_dependency_wait();
+}
+
+// ============================================================ k_shared_combine
+// WR warps per (sequence, query head): fold the records of the prefix segments
+// and of the own parts, 32 at a time: a lane reads one record's maximum and
+// weight sum, then every lane adds its columns of each record under weights
+// that are all known, so that the loads of several records are in flight. One
+// warp per row while there are enough rows, else eight (split_rows in
+// vattn_shared.cu).
+constexpr int kSharedCombWarps = 8;
+
+template <int D, int WR>
 __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const __grid_constant__ SharedParams P) {
-  constexpr int PL = D / 32;
-  __shared__ float s_acc[kSharedCombWarps][D];
+  constexpr int PL = D / 64;  // float2 columns per lane
+  __shared__ float2 s_acc[WR > 1 ? kSharedCombWarps : 1][PL][32];
   __shared__ float2 s_ml[kSharedCombWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  grid_dependency_wait();
   const DevParams& Q = P.D;
-  const int u = blockIdx.x, gh = blockIdx.y;
-  const int b = u / Q.Hkv, h = u % Q.Hkv;
+  const int row_out = blockIdx.x * (kSharedCombWarps / WR) + warp / WR, part = warp % WR;
+  grid_dependency_wait();
+  if (row_out >= Q.batch * Q.Hq) return;  // with WR = 8 the whole CTA
+  const int b = row_out / Q.Hq, hq = row_out % Q.Hq, h = hq / Q.G, gh = hq % Q.G, u = b * Q.Hkv + h;
   const UnitInfo inf = Q.info[u];
-  float* out = Q.out + (static_cast<size_t>(b) * Q.Hq + h * Q.G + gh) * D;
+  float2* out = reinterpret_cast<float2*>(Q.out + static_cast<size_t>(row_out) * D);
   const bool shared = inf.s1 > 0;
   if (inf.n <= 0 || (shared && !P.W.pages_ok[inf.k])) {
-    for (int e = threadIdx.x; e < D; e += blockDim.x) out[e] = 0.0f;
+    if (part == 0)
+      for (int i = 0; i < PL; i++) out[lane + 32 * i] = make_float2(0.0f, 0.0f);
     return;
   }
-  // records of the gather
-  const long long To = Q.pre_det[2 * Q.units];
-  const SliceRecs own = slice_recs(Q.pre_det, 2 * u, To, Q.CD);
+  // records of the own part
+  long long To = 0, own0 = 0;
+  SliceRecs own{0, 0, 0, false};
+  if (P.own_warps) {
+    const int p0 = P.W.own_pre[b];
+    own.n = P.W.own_pre[b + 1] - p0;
+    own0 = static_cast<long long>(p0) * Q.Hkv + static_cast<long long>(h) * own.n;
+  } else {
+    To = Q.pre_det[2 * Q.units];
+    own = slice_recs(Q.pre_det, 2 * u, To, Q.CD);
+  }
   // records of the prefix
   SliceRecs pre{0, 0, 0, false};
   long long Tp = 0, base = 0;
@@ -508,50 +886,101 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
     pre.n = pre.per_item ? g.tiles : cta_of(pre.x0 + g.tiles - 1, Tp, C) - pre.cf + 1;
   }
   const int np = pre.n, N = np + own.n;
-  float m = -INFINITY, l = 0.0f, a[PL];
+  float m = -INFINITY, l = 0.0f;
+  float2 a[PL];
 #pragma unroll
-  for (int i = 0; i < PL; i++) a[i] = 0.0f;
-  for (int j = warp; j < N; j += kSharedCombWarps) {
-    float rm, rl;
-    const float* src;
+  for (int i = 0; i < PL; i++) a[i] = make_float2(0.0f, 0.0f);
+  const int mine = (N - part + WR - 1) / WR;  // records part, part + WR, ...
+  for (int j0 = 0; j0 < mine; j0 += 32) {
+    const int j = j0 + lane < mine ? part + WR * (j0 + lane) : N;
+    float rm = -INFINITY, rl = 0.0f;
+    const float* src = nullptr;
     if (j < np) {
       const long long row = static_cast<long long>(slice_rec(pre, Tp, C, j)) * P.RB + base;
       const float2 v = P.W.ml[row];
       rm = v.x;
       rl = v.y;
       src = P.W.rec + row * D;
-    } else {
-      const long long id = slice_rec(own, To, Q.CD, j - np) + 2LL * u;
-      const float* r = Q.rec_det + static_cast<size_t>(id) * (Q.G * (2 + D)) + gh * (2 + D);
-      rm = r[0] * 1.4426950408889634f;  // the gather keeps natural units
-      rl = r[1];
-      src = r + 2;
+    } else if (j < N) {
+      if (P.own_warps) {
+        const long long id = (own0 + j - np) * Q.G + gh;
+        const float2 v = P.W.own_ml[id];
+        rm = v.x;
+        rl = v.y;
+        src = P.W.own_rec + id * D;
+      } else {
+        const long long id = slice_rec(own, To, Q.CD, j - np);
+        const float* r = Q.rec_det + (id + 2LL * u) * (Q.G * (2 + D)) + gh * (2 + D);
+        rm = r[0] * 1.4426950408889634f;  // the gather keeps natural units
+        rl = r[1];
+        src = r + 2;
+      }
     }
-    if (rl == 0.0f) continue;  // no key, or weights of zero alone
-    const float nm = fmaxf(m, rm);
-    const float fo = exp2f(m - nm), fn = exp2f(rm - nm);
-    l = l * fo + rl * fn;
+    if (rl == 0.0f) rm = -INFINITY;  // no key, or weights of zero alone
+    float top = rm;
 #pragma unroll
-    for (int i = 0; i < PL; i++) a[i] = a[i] * fo + src[lane + 32 * i] * fn;
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == -INFINITY) continue;
+    const float nm = fmaxf(m, top), f = exp2f(m - nm);
     m = nm;
+    const float w = rm == -INFINITY ? 0.0f : exp2f(rm - nm);
+    float sum = rl * w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * f + sum;
+#pragma unroll
+    for (int i = 0; i < PL; i++) {
+      a[i].x *= f;
+      a[i].y *= f;
+    }
+    const int cnt = min(32, mine - j0);
+    for (int k0 = 0; k0 < cnt; k0 += 4) {
+      float2 x[4][PL];
+      float wk[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+        const float* p = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), (k0 + k) & 31));
+#pragma unroll
+        for (int i = 0; i < PL; i++)
+          x[k][i] = k0 + k < cnt && wk[k] != 0.0f ? reinterpret_cast<const float2*>(p)[lane + 32 * i]
+                                                  : make_float2(0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int i = 0; i < PL; i++) {
+          a[i].x += x[k][i].x * wk[k];
+          a[i].y += x[k][i].y * wk[k];
+        }
+    }
+  }
+  if constexpr (WR > 1) {
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+#pragma unroll
+    for (int i = 0; i < PL; i++) s_acc[warp][i][lane] = a[i];
+    __syncthreads();
+    if (part != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WR; w++) top = fmaxf(top, s_ml[w].x);
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PL; i++) a[i] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < WR; w++) {
+      const float f = s_ml[w].x == -INFINITY ? 0.0f : exp2f(s_ml[w].x - top);
+      l += s_ml[w].y * f;
+#pragma unroll
+      for (int i = 0; i < PL; i++) {
+        a[i].x += s_acc[w][i][lane].x * f;
+        a[i].y += s_acc[w][i][lane].y * f;
+      }
+    }
   }
 #pragma unroll
-  for (int i = 0; i < PL; i++) s_acc[warp][lane + 32 * i] = a[i];
-  if (lane == 0) s_ml[warp] = make_float2(m, l);
-  __syncthreads();
-  const int e = threadIdx.x;
-  if (e >= D) return;
-  float M = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kSharedCombWarps; w++) M = fmaxf(M, s_ml[w].x);
-  float A = 0.0f, L = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kSharedCombWarps; w++) {
-    const float f = s_ml[w].x == -INFINITY ? 0.0f : exp2f(s_ml[w].x - M);
-    L += s_ml[w].y * f;
-    A += s_acc[w][e] * f;
-  }
-  out[e] = A / L;
+  for (int i = 0; i < PL; i++) out[lane + 32 * i] = make_float2(a[i].x / l, a[i].y / l);
 }
 
 }  // namespace vattn
