@@ -20,6 +20,12 @@ struct alignas(16) SharedGroup {
   long long tile0, row0;   // key tiles (of every row block and head) and record rows before it
 };
 
+// A piece of a sequence's own positions [start, n): `chunks` chunks of 16 from
+// position `pos` on. id: its index times Hkv, plus the KV head.
+struct alignas(16) OwnPiece {
+  int b, pos, chunks, start, n, id, pad[2];
+};
+
 // Workspace of the shared-prefix decode (see vattn_shared.cuh).
 struct SharedWork {
   int* reach = nullptr;           // [2 max_batch] scratch of k_shared_prep's last two CTAs
@@ -28,9 +34,10 @@ struct SharedWork {
   float* rec = nullptr;           // [record rows][D]
   float2* ml = nullptr;           // [record rows] (maximum in log2 units, weight sum)
   int* own_pre = nullptr;         // [max_batch + 1] prefix sum of own pieces (of one KV head) over sequences
-  int* own_next = nullptr;        // [0]: pieces handed out, [1]: chunks of a piece
-  float* own_rec = nullptr;       // [pieces][G][D]
-  float2* own_ml = nullptr;       // [pieces][G]
+  int* own_next = nullptr;        // pieces (times Hkv) handed out
+  OwnPiece* own_piece = nullptr;  // [pieces]
+  float* own_rec = nullptr;       // [pieces][Hkv][G][D]
+  float2* own_ml = nullptr;       // [pieces][Hkv][G]
   int own_warps = 0;              // warps of k_shared_own (0: not used)
   int grid = 0;                   // CTAs of the prefix kernel
 };

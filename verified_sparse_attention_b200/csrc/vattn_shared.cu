@@ -23,8 +23,7 @@ struct SharedKernels {
   void (*gather)(DevParams);
   unsigned gather_threads;
   size_t gather_smem;
-  void (*combine)(SharedParams);      // one warp per row
-  void (*combine_few)(SharedParams);  // one CTA per row
+  void (*combine[4])(SharedParams);  // 1, 2, 4 or 8 warps per row
 };
 
 template <typename T, int D, int G>
@@ -54,8 +53,10 @@ SharedKernels kernels_for(bool host_kv) {
       k.own_smem = vattn::OwnShape<D>::SMEM;
     }
   }
-  k.combine = vattn::k_shared_combine<D, 1>;
-  k.combine_few = vattn::k_shared_combine<D, vattn::kSharedCombWarps>;
+  k.combine[0] = vattn::k_shared_combine<D, 1>;
+  k.combine[1] = vattn::k_shared_combine<D, 2>;
+  k.combine[2] = vattn::k_shared_combine<D, 4>;
+  k.combine[3] = vattn::k_shared_combine<D, 8>;
   return k;
 }
 
@@ -121,9 +122,10 @@ size_t shared_workspace(vattn_ctx* ctx, char* p) {
   const size_t sz_pre = align256((B + 1) * sizeof(int));
   const size_t sz_rec = align256(rows * c.head_dim * sizeof(float)), sz_ml = align256(rows * sizeof(float2));
   const int own_warps = k.own ? k.own_nw * ctx->num_sms : 0;
-  // at most kOwnPieces pieces per warp, and one more per (sequence, KV head)
-  const size_t own_rows =
-      k.own ? (static_cast<size_t>(vattn::kOwnPieces) * own_warps + B * c.num_kv_heads) * ctx->G : 0;
+  // over the KV heads at most kOwnPieces pieces per warp, and one more per
+  // sequence and head
+  const size_t pieces = k.own ? static_cast<size_t>(vattn::kOwnPieces) * own_warps / c.num_kv_heads + B + 1 : 0;
+  const size_t own_rows = pieces * c.num_q_heads, sz_piece = align256(pieces * sizeof(OwnPiece));
   const size_t sz_orec = align256(own_rows * c.head_dim * sizeof(float)), sz_oml = align256(own_rows * sizeof(float2));
   if (p) {
     SharedWork& w = ctx->shared;
@@ -134,6 +136,7 @@ size_t shared_workspace(vattn_ctx* ctx, char* p) {
     w.ml = reinterpret_cast<float2*>(p); p += sz_ml;
     w.own_pre = reinterpret_cast<int*>(p); p += sz_pre;
     w.own_next = reinterpret_cast<int*>(p); p += 256;
+    w.own_piece = reinterpret_cast<OwnPiece*>(p); p += sz_piece;
     w.own_rec = reinterpret_cast<float*>(p); p += sz_orec;
     w.own_ml = reinterpret_cast<float2*>(p);
     w.own_warps = own_warps;
@@ -142,7 +145,7 @@ size_t shared_workspace(vattn_ctx* ctx, char* p) {
     if (k.own) cudaFuncSetAttribute(k.own, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.own_smem));
     cudaFuncSetAttribute(k.gather, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.gather_smem));
   }
-  return 3 * sz_int + sz_pre + 256 + sz_group + sz_rec + sz_ml + sz_orec + sz_oml;
+  return 3 * sz_int + sz_pre + 256 + sz_piece + sz_group + sz_rec + sz_ml + sz_orec + sz_oml;
 }
 
 }  // namespace vattn
@@ -201,12 +204,11 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
     vattn::launch(k.own, dim3(ctx->num_sms), dim3(k.own_nw * 32), k.own_smem, st, P, &launches);
   else
     vattn::launch(k.gather, dim3(ctx->gather_grid), dim3(k.gather_threads), k.gather_smem, st, P.D, &launches);
-  // a CTA per row while these are resident together (eight per SM), else a
-  // warp per row
+  // as many warps per row as may be resident together (64 per SM)
   const int rows = batch * c.num_q_heads;
-  const bool few = rows <= 8 * ctx->num_sms;
-  vattn::launch(few ? k.combine_few : k.combine,
-                dim3(few ? rows : (rows + vattn::kSharedCombWarps - 1) / vattn::kSharedCombWarps),
-                dim3(vattn::kSharedCombWarps * 32), 0, st, P, &launches);
+  int w = 3;
+  while (w > 0 && (rows << w) > 64 * ctx->num_sms) w--;
+  const int per = vattn::kSharedCombWarps >> w;
+  vattn::launch(k.combine[w], dim3((rows + per - 1) / per), dim3(vattn::kSharedCombWarps * 32), 0, st, P, &launches);
   return vattn::finish(ctx, launches);
 }

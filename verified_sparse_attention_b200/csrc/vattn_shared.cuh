@@ -55,7 +55,7 @@ __device__ __forceinline__ long long block_row0(const SharedParams& P, int mb, i
 // each from the 16-position block that holds `start`. Warps take them in pieces
 // of at least kOwnPiece chunks of one (sequence, KV head), about kOwnPieces a
 // warp when there are many.
-constexpr int kOwnPiece = 8, kOwnPieces = 4;
+constexpr int kOwnPiece = 6, kOwnPieces = 6;
 constexpr int kOwnChunk = 16;
 __device__ __forceinline__ int own_chunks(int start, int n) {
   return n > start ? (n - (start & ~15) + kOwnChunk - 1) / kOwnChunk : 0;
@@ -297,19 +297,46 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
     __syncthreads();
     const long long most = static_cast<long long>(kOwnPieces) * P.own_warps;
     const int piece = static_cast<int>(max(static_cast<long long>(kOwnPiece), (s_carry[1] * D.Hkv + most - 1) / most));
+    __shared__ int s_pre[kSharedPrepKeep + 1];
     for (int base = 0; base < D.batch; base += blockDim.x) {
       const int b = base + tid, start = own_start(b);
       const int cnt = start >= 0 ? (own_chunks(start, len(b)) + piece - 1) / piece : 0;
       const long long carry = s_carry[0], incl = block_scan_ll(cnt, s_w);
-      if (b < D.batch) P.W.own_pre[b] = static_cast<int>(carry + incl - cnt);
+      if (b < D.batch) {
+        const int pre = static_cast<int>(carry + incl - cnt);
+        if (b < kSharedPrepKeep) s_pre[b] = pre;
+        P.W.own_pre[b] = pre;
+      }
       __syncthreads();
       if (tid == blockDim.x - 1) s_carry[0] = carry + incl;
       __syncthreads();
     }
+    const int total = static_cast<int>(s_carry[0]);
     if (tid == 0) {
-      P.W.own_pre[D.batch] = static_cast<int>(s_carry[0]);
+      P.W.own_pre[D.batch] = total;
       P.W.own_next[0] = 0;
-      P.W.own_next[1] = piece;
+    }
+    __threadfence_block();
+    __syncthreads();
+    auto pre_of = [&](int b) -> int {
+      return b < kSharedPrepKeep ? s_pre[b] : *static_cast<volatile int*>(&P.W.own_pre[b]);
+    };
+    // the pieces themselves
+    for (int j = tid; j < total; j += blockDim.x) {
+      int lo = 0, hi = D.batch;  // the last sequence whose pieces begin at or before j
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (pre_of(mid) <= j) lo = mid;
+        else hi = mid;
+      }
+      const int first = (j - pre_of(lo)) * piece, start = own_start(lo), n = len(lo);
+      OwnPiece e = {};
+      e.b = lo;
+      e.pos = (start & ~15) + kOwnChunk * first;
+      e.chunks = min(piece, own_chunks(start, n) - first);
+      e.start = start;
+      e.n = n;
+      P.W.own_piece[j] = e;
     }
     return;
   }
@@ -553,8 +580,8 @@ __global__ void __launch_bounds__(256, 1) k_shared_prefix(const __grid_constant_
 // filled NS - 1 chunks ahead of the one being computed, across the ends of
 // runs, by two or four tensor copies a chunk. SMs stream at rates that differ
 // by a third, and the prefix kernel leaves them at different times, so warps
-// take pieces of runs from a counter (the first by their index); a piece has
-// the record of its index. The arithmetic of a chunk is k_gather_tc's: S = K q
+// take pieces of runs from a counter (the first by their index; the KV heads of
+// a piece follow one another); a piece has the record of its index. The arithmetic of a chunk is k_gather_tc's: S = K q
 // as m16n8k16 products, the online softmax in the accumulator layout,
 // O^T += V^T P with the weights as two bf16 terms.
 // The kernel needs k_shared_prep's results alone: it starts while the prefix
@@ -571,46 +598,9 @@ struct OwnShape {
   static constexpr int NS = D == 128 ? 4 : 6;
   static constexpr int QUEUE = 8;                    // pieces between the copies and the arithmetic: at most NS + 1
   static constexpr size_t RING = static_cast<size_t>(NW) * NS * STAGE;
-  static constexpr size_t SMEM = RING + static_cast<size_t>(NW) * (NS * 8 + QUEUE * 24);
+  static constexpr size_t SMEM = RING + static_cast<size_t>(NW) * (NS * 8 + QUEUE * sizeof(OwnPiece));
   static_assert(NS + 1 <= QUEUE && SMEM <= 227 * 1024, "shared memory of the own part");
 };
-
-__device__ __forceinline__ UnitInfo load_info(const UnitInfo* p) {
-  UnitInfo inf;
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(UnitInfo) / 16); i++)
-    reinterpret_cast<int4*>(&inf)[i] = __ldcg(reinterpret_cast<const int4*>(p) + i);
-  return inf;
-}
-
-// A piece of a run: `chunks` chunks from position `pos` of unit u, whose own
-// positions are [start, n).
-struct OwnPiece {
-  int id, u, pos, chunks, start, n;
-};
-__device__ __forceinline__ OwnPiece own_piece(const SharedParams& P, int id, int per) {
-  const DevParams& Q = P.D;
-  const int lane = threadIdx.x & 31;
-  // the last sequence whose pieces begin at or before id, 32 probes at a time
-  int lo = 0, hi = Q.batch;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, i < hi && __ldcg(&P.W.own_pre[i]) * Q.Hkv <= id);
-    lo += (__popc(le) - 1) * step;
-    hi = min(lo + step, hi);
-  }
-  const int p0 = __ldcg(&P.W.own_pre[lo]), cnt = __ldcg(&P.W.own_pre[lo + 1]) - p0;
-  const UnitInfo inf = load_info(Q.info + static_cast<size_t>(lo) * Q.Hkv);
-  const int y = id - p0 * Q.Hkv, h = y / cnt, first = (y - h * cnt) * per;
-  OwnPiece r;
-  r.id = id;
-  r.u = lo * Q.Hkv + h;
-  r.pos = (inf.s1 & ~15) + kOwnChunk * first;
-  r.chunks = max(min(per, own_chunks(inf.s1, inf.n) - first), 0);  // none of a sequence that failed
-  r.start = inf.s1;
-  r.n = inf.n;
-  return r;
-}
 
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
@@ -635,52 +625,66 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
   if (lane < NS) mbar_init(&bars[lane], 1);
   mbar_init_fence();
   __syncwarp();
-  const int total = __ldcg(&P.W.own_pre[Q.batch]) * Q.Hkv, per = __ldcg(&P.W.own_next[1]);
+  const int total = __ldcg(&P.W.own_pre[Q.batch]) * Q.Hkv;
   const float c = Q.scale * 1.4426950408889634f;  // scores in log2 units
 
   if (gw < total) {
-    // producer: the piece being copied, its next chunk and that chunk's page;
-    // the piece after it
-    OwnPiece pp = own_piece(P, gw, per), pn = pp;
-    bool more = true;         // pn is a piece still to come
-    int px = 0;
+    // Producer: the piece being copied (pp), its next chunk and that chunk's
+    // page, and the piece after it (pn), which is fetched in three dependent
+    // steps, one with every chunk copied: its index, its entry, its state and
+    // first page.
+    OwnPiece pp, pn;
+    int px = 0, page = 0, id_n = gw, page_n = 0, n_n = 0, step = 1;
     unsigned nq = 0, dq = 0;  // pieces queued and taken
     unsigned ni = 0, nc = 0;  // chunks copied and computed (stage and phase follow)
     auto page_of = [&](const OwnPiece& p, int x) -> int {
-      const int pos = p.pos + kOwnChunk * x;
-      return __ldcg(Q.page_table + static_cast<size_t>(p.u / Q.Hkv) * Q.pps + page_slot(Q, pos));
+      return __ldcg(Q.page_table + static_cast<size_t>(p.b) * Q.pps + page_slot(Q, p.pos + kOwnChunk * x));
     };
-    auto fetch = [&]() {
-      int id = 0;
-      if (lane == 0) id = W + atomicAdd(&P.W.own_next[0], 1);
-      id = __shfl_sync(0xffffffffu, id, 0);
-      more = id < total;
-      if (more) pn = own_piece(P, id, per);
+    auto fetch_step = [&]() {  // 0 -> 3; 4: no piece is left
+      if (step == 0) {
+        if (lane == 0) id_n = W + atomicAdd(&P.W.own_next[0], 1);
+        step = 1;
+      } else if (step == 1) {
+        id_n = __shfl_sync(0xffffffffu, id_n, 0);
+        step = id_n < total ? 2 : 4;
+        if (step == 2) {
+          const int4* e = reinterpret_cast<const int4*>(&P.W.own_piece[id_n / Q.Hkv]);
+          const int4 a = __ldcg(e), b = __ldcg(e + 1);
+          pn.b = a.x;
+          pn.pos = a.y;
+          pn.chunks = a.z;
+          pn.start = a.w;
+          pn.n = b.x;
+          pn.id = id_n;
+        }
+      } else if (step == 2) {
+        n_n = __ldcg(&Q.info[static_cast<size_t>(pn.b) * Q.Hkv].n);
+        page_n = page_of(pn, 0);
+        step = 3;
+      }
     };
-    auto enqueue = [&]() {
-      if (pp.chunks == 0) return;
+    // the next piece that can be read becomes the one being copied
+    auto advance = [&]() -> bool {
+      do {
+        while (step < 3) fetch_step();
+        if (step == 4) return false;
+        pp = pn;
+        step = 0;
+      } while (n_n <= 0);  // a sequence whose pages failed
+      px = 0;
+      page = page_n;
       if (lane == 0) queue[nq % S::QUEUE] = pp;
       __syncwarp();
       nq++;
+      return true;
     };
-    int page = pp.chunks > 0 ? page_of(pp, 0) : 0, page_n = 0;
-    auto fetch_page = [&]() { page_n = more && pn.chunks > 0 ? page_of(pn, 0) : 0; };
-    enqueue();
-    fetch();
-    fetch_page();
+    bool left = advance();
     auto issue = [&]() {  // one chunk, if there is one and a stage is free
       if (ni - nc >= NS) return;
-      while (px >= pp.chunks) {
-        if (!more) return;
-        pp = pn;
-        px = 0;
-        page = page_n;
-        enqueue();
-        fetch();
-        fetch_page();
-      }
+      if (left && px >= pp.chunks) left = advance();
+      if (!left) return;
       const int pos = pp.pos + kOwnChunk * px;
-      const int row = (page * Q.Hkv + pp.u % Q.Hkv) * Q.ps + (pos - page_slot(Q, pos) * Q.ps);
+      const int row = (page * Q.Hkv + pp.id % Q.Hkv) * Q.ps + (pos - page_slot(Q, pos) * Q.ps);
       const int st = static_cast<int>(ni % NS);
       fence_proxy_async();  // the stage's earlier reads come before the copy's writes
       if (lane == 0) mbar_arrive_expect_tx(&bars[st], STAGE);
@@ -690,6 +694,7 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
       ni++;
       px++;
       if (px < pp.chunks) page = page_of(pp, px);
+      if (step < 3) fetch_step();
     };
 #pragma unroll 1
     for (int i = 0; i < NS - 1; i++) issue();
@@ -705,8 +710,7 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
       unsigned qf[KT][2];
       {
         const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(Q.q) +
-                                  (static_cast<size_t>(cu.u / Q.Hkv) * Q.Hq + (cu.u % Q.Hkv) * G + (ra < G ? ra : 0)) * D +
-                                  hc;
+                                  (static_cast<size_t>(cu.b) * Q.Hq + (cu.id % Q.Hkv) * G + (ra < G ? ra : 0)) * D + hc;
 #pragma unroll
         for (int kt = 0; kt < KT; kt++)
 #pragma unroll
@@ -835,9 +839,7 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
 // WR warps per (sequence, query head): fold the records of the prefix segments
 // and of the own parts, 32 at a time: a lane reads one record's maximum and
 // weight sum, then every lane adds its columns of each record under weights
-// that are all known, so that the loads of several records are in flight. One
-// warp per row while there are enough rows, else eight (split_rows in
-// vattn_shared.cu).
+// that are all known, so that the loads of several records are in flight.
 constexpr int kSharedCombWarps = 8;
 
 template <int D, int WR>
@@ -849,23 +851,18 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
   const DevParams& Q = P.D;
   const int row_out = blockIdx.x * (kSharedCombWarps / WR) + warp / WR, part = warp % WR;
   grid_dependency_wait();
-  if (row_out >= Q.batch * Q.Hq) return;  // with WR = 8 the whole CTA
-  const int b = row_out / Q.Hq, hq = row_out % Q.Hq, h = hq / Q.G, gh = hq % Q.G, u = b * Q.Hkv + h;
+  const bool real = row_out < Q.batch * Q.Hq;
+  const int b = real ? row_out / Q.Hq : 0, hq = row_out % Q.Hq, h = hq / Q.G, gh = hq % Q.G, u = b * Q.Hkv + h;
   const UnitInfo inf = Q.info[u];
   float2* out = reinterpret_cast<float2*>(Q.out + static_cast<size_t>(row_out) * D);
   const bool shared = inf.s1 > 0;
-  if (inf.n <= 0 || (shared && !P.W.pages_ok[inf.k])) {
-    if (part == 0)
-      for (int i = 0; i < PL; i++) out[lane + 32 * i] = make_float2(0.0f, 0.0f);
-    return;
-  }
+  const bool none = inf.n <= 0 || (shared && !P.W.pages_ok[inf.k]);
   // records of the own part
   long long To = 0, own0 = 0;
   SliceRecs own{0, 0, 0, false};
   if (P.own_warps) {
-    const int p0 = P.W.own_pre[b];
-    own.n = P.W.own_pre[b + 1] - p0;
-    own0 = static_cast<long long>(p0) * Q.Hkv + static_cast<long long>(h) * own.n;
+    own0 = P.W.own_pre[b];
+    own.n = P.W.own_pre[b + 1] - static_cast<int>(own0);
   } else {
     To = Q.pre_det[2 * Q.units];
     own = slice_recs(Q.pre_det, 2 * u, To, Q.CD);
@@ -885,7 +882,7 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
     pre.cf = pre.per_item ? 0 : cta_of(pre.x0, Tp, C);
     pre.n = pre.per_item ? g.tiles : cta_of(pre.x0 + g.tiles - 1, Tp, C) - pre.cf + 1;
   }
-  const int np = pre.n, N = np + own.n;
+  const int np = pre.n, N = real && !none ? np + own.n : 0;
   float m = -INFINITY, l = 0.0f;
   float2 a[PL];
 #pragma unroll
@@ -903,7 +900,7 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
       src = P.W.rec + row * D;
     } else if (j < N) {
       if (P.own_warps) {
-        const long long id = (own0 + j - np) * Q.G + gh;
+        const long long id = ((own0 + j - np) * Q.Hkv + h) * Q.G + gh;
         const float2 v = P.W.own_ml[id];
         rm = v.x;
         rl = v.y;
@@ -934,11 +931,12 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
       a[i].y *= f;
     }
     const int cnt = min(32, mine - j0);
-    for (int k0 = 0; k0 < cnt; k0 += 4) {
-      float2 x[4][PL];
-      float wk[4];
+    constexpr int B = 4;  // records whose loads are in flight together (8: slower by 1 to 6 us, fewer warps fit)
+    for (int k0 = 0; k0 < cnt; k0 += B) {
+      float2 x[B][PL];
+      float wk[B];
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
+      for (int k = 0; k < B; k++) {
         wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
         const float* p = reinterpret_cast<const float*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), (k0 + k) & 31));
@@ -948,7 +946,7 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
                                                   : make_float2(0.0f, 0.0f);
       }
 #pragma unroll
-      for (int k = 0; k < 4; k++)
+      for (int k = 0; k < B; k++)
 #pragma unroll
         for (int i = 0; i < PL; i++) {
           a[i].x += x[k][i].x * wk[k];
@@ -964,23 +962,25 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
     if (part != 0) return;
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < WR; w++) top = fmaxf(top, s_ml[w].x);
+    for (int w = 0; w < WR; w++) top = fmaxf(top, s_ml[warp + w].x);
     l = 0.0f;
 #pragma unroll
     for (int i = 0; i < PL; i++) a[i] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < WR; w++) {
-      const float f = s_ml[w].x == -INFINITY ? 0.0f : exp2f(s_ml[w].x - top);
-      l += s_ml[w].y * f;
+      const float f = s_ml[warp + w].x == -INFINITY ? 0.0f : exp2f(s_ml[warp + w].x - top);
+      l += s_ml[warp + w].y * f;
 #pragma unroll
       for (int i = 0; i < PL; i++) {
-        a[i].x += s_acc[w][i][lane].x * f;
-        a[i].y += s_acc[w][i][lane].y * f;
+        a[i].x += s_acc[warp + w][i][lane].x * f;
+        a[i].y += s_acc[warp + w][i][lane].y * f;
       }
     }
   }
+  if (!real) return;
 #pragma unroll
-  for (int i = 0; i < PL; i++) out[lane + 32 * i] = make_float2(a[i].x / l, a[i].y / l);
+  for (int i = 0; i < PL; i++)
+    out[lane + 32 * i] = none ? make_float2(0.0f, 0.0f) : make_float2(a[i].x / l, a[i].y / l);
 }
 
 }  // namespace vattn
