@@ -386,8 +386,13 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       for (int i = 0; i < steps && ok; i++) {
         const int kt = two ? i : 2 * i + st;
         const int nk = s.prefix - (s.t0 + kt) * KT;
+        ok = __all_sync(0xffffffffu, mbar_wait(&tail.s[st], ns & 1u));
+        ns++;
+        if (!ok) break;
         if (nk < KT && (!two || st == 0)) {
-          // the V rows behind the prefix's last key: zero, whatever the cache holds
+          // the V rows behind the prefix's last key: zero, whatever the cache holds.
+          // (The tile's scores are there, so every earlier use of V's ring tile is
+          // over and its barrier is in the phase waited for, or past it.)
           const unsigned idx = li0 + 2u * kt + 1u, slot = idx % NST;
           ok = __all_sync(0xffffffffu, mbar_wait(&tail.full[slot], (idx / NST) & 1u));
           if (!ok) break;
@@ -397,9 +402,6 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
               *reinterpret_cast<uint4*>(s_ring + slot * TILE + hf * HALF + x * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async();
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&tail.s[st], ns & 1u));
-        ns++;
-        if (!ok) break;
         tc_fence_after();
         // the row's 128 scores in four chunks of 32: the maximum over all; the
         // first two stay in registers, the others are read again (their weights
