@@ -178,7 +178,8 @@ struct AppendArgs {
   const int *page_table, *seq_lens, *cu;
   unsigned* err;
   int tokens, batch, Hq, Hkv, ps, pps, max_ctx, num_pages;
-  int key_blocks;        // proxies: blocks that take one head of a tile of tokens each
+  int key_blocks;        // proxies: blocks that take key_heads heads of a tile of tokens each
+  int key_heads;
   int lanes, tok_block;  // as in RotateArgs
   int row_y;             // blocks that share a token's rows
 };
@@ -186,7 +187,7 @@ struct AppendArgs {
 // Position and cache row (page * Hkv * ps + slot; -1: nothing to write) of
 // tokens [t0, t0 + n) into shared memory, by the whole block. Every sequence
 // marks its own tokens of the range, in one round of loads.
-__device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_pos, long long* s_row) {
+__device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_pos, int* s_row) {
   if (A.cu != nullptr) {
     for (int i = threadIdx.x; i < n; i += blockDim.x) s_seq[i] = -1;
     __syncthreads();
@@ -211,7 +212,7 @@ __device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_p
     __syncthreads();
   }
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    long long row = -1;
+    int row = -1;  // below 2^31, as the host checked
     int b, pos;
     if (A.cu != nullptr) {
       b = s_seq[i];
@@ -231,76 +232,195 @@ __device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_p
       if (page < 0 || page >= A.num_pages)
         atomicOr(A.err, kDevBadPage);
       else
-        row = static_cast<long long>(page) * A.Hkv * A.ps + (pos - slot * A.ps);
+        row = page * A.Hkv * A.ps + (pos - slot * A.ps);
     }
     s_row[i] = row;
   }
   __syncthreads();
 }
 
-// Tokens of a key tile: its stored keys stay in shared memory for the
-// transposed or projected copy.
-template <typename T>
-constexpr int kKeyTile = sizeof(T) == 2 ? 64 : 32;
+// Keys with a proxy copy: a block takes a tile of TT tokens and some of the
+// heads, keeps the tokens' cosines in registers over the heads, and the stored
+// (rounded) keys of one head in shared memory for the copy while the next
+// head's are loaded.
+template <typename T, int D, int E, int PROXY>
+struct KeyTile {
+  static constexpr int NP = D / (2 * E);
+  static constexpr int TT = E > 1 ? kThreads / NP : 32;  // vectors: one chunk pair per thread
+  // row pitch: odd in words for the transposed copy's column reads, 16-byte
+  // rows for the projection's fragment loads
+  static constexpr int LD = PROXY == VATTN_SPARQ ? D + 4 / sizeof(T) : D + 16 / sizeof(T);
+};
+
+__device__ __forceinline__ unsigned smem_addr(const void* p) { return static_cast<unsigned>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void ldsm4(unsigned addr, unsigned (&a)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ unsigned pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const unsigned*>(&v);
+}
+
+// Projected keys of a tile of bf16 keys: [TT tokens x D] . [D x 32] on the
+// tensor cores, the fp32 basis as two bf16 terms: 2^-18 of the summed magnitudes
+// is lost, against the 2^-9 of the bf16 result's own rounding. Every warp has 16
+// tokens and 4 TT / 16 components; the basis comes straight from L2 in operand
+// order. As fp32 FMAs from shared memory a call of 8190 tokens took 73 us.
+template <int D, int LD, int TT>
+__device__ __forceinline__ void project_tile(const __nv_bfloat16* s_key, const float* basis, const int* s_row, int n,
+                                             int h, const AppendArgs& A) {
+  constexpr int MT = TT / 16, NX = 4 * MT / 8;  // token tiles; 8-component tiles of a warp
+  static_assert(kThreads / 32 * NX == 4 * MT && NX >= 1, "warps cover the tile");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int m0 = 16 * (warp % MT), n0 = 8 * NX * (warp / MT);
+  if (m0 >= n) return;
+  float acc[NX][4];
+#pragma unroll
+  for (int x = 0; x < NX; x++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) acc[x][i] = 0.0f;
+  const unsigned rows = smem_addr(s_key + (m0 + (lane & 15)) * LD + (lane >> 4) * 8);
+  const float* bp = basis + (2 * (lane & 3)) * kRank + n0 + (lane >> 2);
+#pragma unroll
+  for (int k = 0; k < D; k += 16) {
+    unsigned a[4];
+    ldsm4(rows + k * 2, a);
+#pragma unroll
+    for (int x = 0; x < NX; x++) {
+      float b[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) b[i] = __ldg(bp + (k + (i & 1) + 8 * (i >> 1)) * kRank + 8 * x);
+      const unsigned b0 = pack2(b[0], b[1]), b1 = pack2(b[2], b[3]);
+      mma16816(acc[x], a, b0, b1);
+      mma16816(acc[x], a,
+               pack2(b[0] - __uint_as_float(b0 << 16), b[1] - __uint_as_float(b0 & 0xFFFF0000u)),
+               pack2(b[2] - __uint_as_float(b1 << 16), b[3] - __uint_as_float(b1 & 0xFFFF0000u)));
+    }
+  }
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.k_proj);
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+    const int i = m0 + (lane >> 2) + 8 * half;
+    if (i >= n || s_row[i] < 0) continue;
+    unsigned* o =
+        reinterpret_cast<unsigned*>(out + static_cast<size_t>(s_row[i] + h * A.ps) * kRank + n0 + 2 * (lane & 3));
+#pragma unroll
+    for (int x = 0; x < NX; x++) o[4 * x] = pack2(acc[x][2 * half], acc[x][2 * half + 1]);
+  }
+}
+// The same of fp32 keys: fp32 FMAs, four tokens per thread.
+template <int D, int LD, int TT>
+__device__ __forceinline__ void project_tile(const float* s_key, const float* basis, const int* s_row, int n, int h,
+                                             const AppendArgs& A) {
+  static_assert(TT <= kThreads / kRank * 4, "threads cover the tile");
+  const int r = threadIdx.x % kRank, i0 = threadIdx.x / kRank * 4;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (i0 >= n) return;
+#pragma unroll 4
+  for (int j = 0; j < D; j += 4) {
+    float b[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) b[e] = __ldg(basis + (j + e) * kRank + r);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float4 k = *reinterpret_cast<const float4*>(s_key + (i0 + i) * LD + j);
+      acc[i] = fmaf(k.x, b[0], acc[i]);
+      acc[i] = fmaf(k.y, b[1], acc[i]);
+      acc[i] = fmaf(k.z, b[2], acc[i]);
+      acc[i] = fmaf(k.w, b[3], acc[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    if (i0 + i < n && s_row[i0 + i] >= 0)
+      static_cast<float*>(A.k_proj)[static_cast<size_t>(s_row[i0 + i] + h * A.ps) * kRank + r] =
+          acc[i];
+}
 
 template <typename T, int D, int E, int PROXY>
 __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ AppendArgs A) {
   constexpr int NP = D / (2 * E);
   __shared__ int s_seq[kMaxTok], s_pos[kMaxTok];
-  __shared__ long long s_row[kMaxTok];
+  __shared__ int s_row[kMaxTok];
   dependency_wait();
   int blk = blockIdx.x;
   if constexpr (PROXY != VATTN_EXACT) {
     if (blk < A.key_blocks) {
-      constexpr int TT = kKeyTile<T>;
-      constexpr int PAD = 16 / sizeof(T) + 4 / sizeof(T);
-      __shared__ __align__(16) T s_key[TT][D + PAD];
-      const int h = blk % A.Hkv, t0 = blk / A.Hkv * TT;
+      using S = KeyTile<T, D, E, PROXY>;
+      constexpr int TT = S::TT, LD = S::LD, LANES = kThreads / NP;  // LANES: tokens at once
+      constexpr bool kOnce = TT <= LANES;                           // every thread has one token
+      __shared__ __align__(16) T s_key[2][TT * LD];
+      const int splits = (A.Hkv + A.key_heads - 1) / A.key_heads;
+      const int h0 = blk % splits * A.key_heads, h1 = min(A.Hkv, h0 + A.key_heads), t0 = blk / splits * TT;
       const int n = min(TT, A.tokens - t0);
       resolve(A, t0, n, s_seq, s_pos, s_row);
-      const int p = threadIdx.x % NP;
+      const int p = threadIdx.x % NP, lane0 = threadIdx.x / NP;
       Pair<T, D, E> P;
       P.place(A.rope, p);
-      for (int i = threadIdx.x / NP; i < n; i += kThreads / NP) {
-        if (s_row[i] < 0) continue;
-        P.turn(A.rope, p, s_pos[i], false);
+      const bool mine = lane0 < n && s_row[lane0] >= 0;
+      Chunk<T, E> na, nb;
+      auto load = [&](int i, int h, Chunk<T, E>& ca, Chunk<T, E>& cb) {
         const T* x = static_cast<const T*>(A.k) + (t0 + i) * A.ks + h * D;
-        Chunk<T, E> ca, cb;
         ca.load(x + P.a);
         cb.load(x + P.b);
-        if (P.turned) P.apply(ca, cb);
-        T* o = static_cast<T*>(A.k_cache) + static_cast<size_t>(s_row[i] + h * A.ps) * D;
-        ca.store(o + P.a);
-        cb.store(o + P.b);
-        const T* ra = reinterpret_cast<const T*>(&ca.raw);
-        const T* rb = reinterpret_cast<const T*>(&cb.raw);
-#pragma unroll
-        for (int e = 0; e < E; e++) {
-          s_key[i][P.a + e] = ra[e];
-          s_key[i][P.b + e] = rb[e];
-        }
+      };
+      if (kOnce && mine) {
+        load(lane0, h0, na, nb);
+        P.turn(A.rope, p, s_pos[lane0], false);
       }
-      __syncthreads();
-      if constexpr (PROXY == VATTN_SPARQ) {
-        // neighbouring lanes hold neighbouring tokens, whose slots are neighbours too
-        const int i = threadIdx.x % TT;
-        if (i >= n || s_row[i] < 0) return;
-        // row = page * Hkv * ps + slot: the page's dim-major block starts at (page * Hkv + h) * D * ps
-        const long long head = s_row[i] / A.ps + h, slot = s_row[i] % A.ps;
-        T* o = static_cast<T*>(A.k_t) + static_cast<size_t>(head) * D * A.ps + slot;
-        for (int j = threadIdx.x / TT; j < D; j += kThreads / TT) o[static_cast<size_t>(j) * A.ps] = s_key[i][j];
-      } else {
-        __shared__ __align__(16) float s_basis[D][kRank];
-        const float* basis = A.basis + static_cast<size_t>(h) * D * kRank;
-        for (int i = threadIdx.x; i < D * kRank; i += kThreads) (&s_basis[0][0])[i] = basis[i];
-        __syncthreads();
-        for (int x = threadIdx.x; x < n * kRank; x += kThreads) {
-          const int i = x / kRank, r = x % kRank;
-          if (s_row[i] < 0) continue;
-          float acc = 0.0f;
+      for (int h = h0; h < h1; h++) {
+        T* key = s_key[(h - h0) & 1];
+        auto put = [&](int i, Chunk<T, E>& ca, Chunk<T, E>& cb) {
+          if (P.turned) P.apply(ca, cb);
+          T* o = static_cast<T*>(A.k_cache) + static_cast<size_t>(s_row[i] + h * A.ps) * D;
+          ca.store(o + P.a);
+          cb.store(o + P.b);
+          const T* ra = reinterpret_cast<const T*>(&ca.raw);
+          const T* rb = reinterpret_cast<const T*>(&cb.raw);
+#pragma unroll
+          for (int e = 0; e < E; e++) {
+            key[i * LD + P.a + e] = ra[e];
+            key[i * LD + P.b + e] = rb[e];
+          }
+        };
+        if constexpr (kOnce) {
+          if (mine) {
+            Chunk<T, E> ca = na, cb = nb;
+            if (h + 1 < h1) load(lane0, h + 1, na, nb);
+            put(lane0, ca, cb);
+          }
+        } else {
+          for (int i = lane0; i < n; i += LANES) {
+            if (s_row[i] < 0) continue;
+            P.turn(A.rope, p, s_pos[i], false);
+            Chunk<T, E> ca, cb;
+            load(i, h, ca, cb);
+            put(i, ca, cb);
+          }
+        }
+        __syncthreads();  // (the other buffer's readers have passed the sync before)
+        if constexpr (PROXY == VATTN_SPARQ) {
+          // neighbouring lanes hold neighbouring tokens, whose slots are neighbours too
+          const int i = threadIdx.x % TT;
+          if (i < n && s_row[i] >= 0) {
+            // row = page * Hkv * ps + slot: the head's dim-major block starts at (page * Hkv + h) * D * ps
+            const int head = s_row[i] / A.ps + h, slot = s_row[i] % A.ps;
+            T* o = static_cast<T*>(A.k_t) + static_cast<size_t>(head) * D * A.ps + slot;
 #pragma unroll 8
-          for (int j = 0; j < D; j++) acc = fmaf(static_cast<float>(s_key[i][j]), s_basis[j][r], acc);
-          static_cast<T*>(A.k_proj)[static_cast<size_t>(s_row[i] + h * A.ps) * kRank + r] = static_cast<T>(acc);
+            for (int j = threadIdx.x / TT; j < D; j += kThreads / TT) o[static_cast<size_t>(j) * A.ps] = key[i * LD + j];
+          }
+        } else {
+          project_tile<D, LD, TT>(key, A.basis + static_cast<size_t>(h) * D * kRank, s_row, n, h, A);
         }
       }
       return;
@@ -323,7 +443,7 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
   P.place(A.rope, p);
   P.turn(A.rope, p, s_pos[i], false);
   const long long t = t0 + i;
-  const long long row = s_row[i];
+  const int row = s_row[i];
   // rows in the order keys, queries, values
   const int nq = rows - A.Hkv;
   auto src = [&](int r) -> const T* {
@@ -332,9 +452,9 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
     return static_cast<const T*>(A.v) + t * A.vs + (r - nq) * D;
   };
   auto dst = [&](int r) -> T* {
-    if (r < nk) return static_cast<T*>(A.k_cache) + static_cast<size_t>(row + static_cast<long long>(r) * A.ps) * D;
+    if (r < nk) return static_cast<T*>(A.k_cache) + static_cast<size_t>(row + r * A.ps) * D;
     if (r < nq) return static_cast<T*>(A.q_out) + (t * A.Hq + (r - nk)) * D;
-    return static_cast<T*>(A.v_cache) + static_cast<size_t>(row + static_cast<long long>(r - nq) * A.ps) * D;
+    return static_cast<T*>(A.v_cache) + static_cast<size_t>(row + (r - nq) * A.ps) * D;
   };
   for (int r = r0; r < rows; r += kUnroll * A.lanes) {
     Chunk<T, E> ca[kUnroll], cb[kUnroll];
@@ -421,10 +541,16 @@ int run_append(AppendArgs& a, bool vec, int sms, cudaStream_t st) {
   a.tok_block = s.tok_block;
   a.row_y = s.row_y;
   a.key_blocks = 0;
-  if (PROXY != VATTN_EXACT) {
-    const long long tiles = (a.tokens + kKeyTile<T> - 1) / kKeyTile<T>;
-    if (tiles * a.Hkv > 0x3FFFFFFFLL) return VATTN_EINVAL;
-    a.key_blocks = static_cast<int>(tiles * a.Hkv);
+  a.key_heads = 1;
+  if constexpr (PROXY != VATTN_EXACT) {
+    // as many heads per block as still leave four blocks for every SM
+    const int TT = vec ? KeyTile<T, D, E, PROXY>::TT : KeyTile<T, D, 1, PROXY>::TT;
+    const long long tiles = (a.tokens + TT - 1) / TT;
+    a.key_heads = static_cast<int>(
+        std::max(1LL, std::min<long long>(a.Hkv, tiles * a.Hkv / (4LL * sms))));
+    const long long blocks = tiles * ((a.Hkv + a.key_heads - 1) / a.key_heads);
+    if (blocks > 0x3FFFFFFFLL) return VATTN_EINVAL;
+    a.key_blocks = static_cast<int>(blocks);
   }
   const long long gx = a.key_blocks + static_cast<long long>((a.tokens + s.tok_block - 1) / s.tok_block) * s.row_y;
   if (gx > 0x7FFFFFFFLL) return VATTN_EINVAL;
