@@ -233,8 +233,7 @@ struct AppendArgs {
   const int *page_table, *seq_lens, *cu;
   unsigned* err;
   int tokens, batch, Hq, Hkv, ps, pps, max_ctx, num_pages;
-  int key_blocks;        // proxies: blocks that take key_heads heads of a tile of tokens each
-  int key_heads;
+  int key_blocks;        // proxies: blocks that take the keys and values
   int lanes, tok_block;  // as in RotateArgs
   int row_y;             // blocks that share a token's rows
 };
@@ -294,10 +293,11 @@ __device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_p
   __syncthreads();
 }
 
-// Keys with a proxy copy, and the values beside them: a block takes a tile of
-// TT tokens and some of the heads, keeps the tokens' cosines in registers over
-// the heads, and the stored (rounded) keys of one head in shared memory for the
-// copy while the next head's rows are loaded.
+// Keys with a proxy copy, and the values beside them. The jobs (tile of TT
+// tokens, KV head) are cut evenly over about as many blocks as are resident; a
+// block keeps a tile's cosines in registers over its heads, and the stored
+// (rounded) keys of one job in shared memory for the copy while the next job's
+// rows are loaded.
 template <typename T, int D, int E, int PROXY>
 struct KeyTile {
   static constexpr int NP = D / (2 * E);
@@ -415,27 +415,39 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
       constexpr int TT = S::TT, LD = S::LD, LANES = kThreads / NP;  // LANES: tokens at once
       constexpr bool kOnce = TT <= LANES;                           // every thread has one token
       __shared__ __align__(16) T s_key[2][TT * LD];
-      const int splits = (A.Hkv + A.key_heads - 1) / A.key_heads;
-      const int h0 = blk % splits * A.key_heads, h1 = min(A.Hkv, h0 + A.key_heads), t0 = blk / splits * TT;
-      const int n = min(TT, A.tokens - t0);
+      const int jobs = (A.tokens + TT - 1) / TT * A.Hkv;
+      const int j0 = static_cast<int>(static_cast<long long>(jobs) * blk / A.key_blocks);
+      const int j1 = static_cast<int>(static_cast<long long>(jobs) * (blk + 1) / A.key_blocks);
       const int p = threadIdx.x % NP, lane0 = threadIdx.x / NP;
       Pair<T, D, E> P;
       P.place(A.rope, p);
-      Chunk<T, E> next[4];  // the key's and the value's chunk pair of the next head
-      auto load = [&](int i, int h, Chunk<T, E> (&c)[4]) {
-        const T* x = static_cast<const T*>(A.k) + (t0 + i) * A.ks + h * D;
-        const T* y = static_cast<const T*>(A.v) + (t0 + i) * A.vs + h * D;
+      Chunk<T, E> next[4];  // the key's and the value's chunk pair of the next job
+      auto load = [&](int t, int h, Chunk<T, E> (&c)[4]) {
+        const T* x = static_cast<const T*>(A.k) + t * A.ks + h * D;
+        const T* y = static_cast<const T*>(A.v) + t * A.vs + h * D;
         c[0].load(x + P.a);
         c[1].load(x + P.b);
         c[2].load(y + P.a);
         c[3].load(y + P.b);
       };
-      if (kOnce && lane0 < n) load(lane0, h0, next);  // in flight while positions and pages are found
-      resolve(A, t0, n, s_seq, s_pos, s_row);
-      const bool mine = lane0 < n && s_row[lane0] >= 0;
-      if (kOnce && mine) P.turn(A.rope, p, s_pos[lane0], false);
-      for (int h = h0; h < h1; h++) {
-        T* key = s_key[(h - h0) & 1];
+      auto load_next = [&](int j) {
+        const long long t = static_cast<long long>(j / A.Hkv) * TT + lane0;
+        if (kOnce && j < j1 && lane0 < TT && t < A.tokens) load(static_cast<int>(t), j % A.Hkv, next);
+      };
+      load_next(j0);  // in flight while positions and pages are found
+      int tile = -1, n = 0;
+      bool mine = false;
+      for (int j = j0; j < j1; j++) {
+        const int h = j % A.Hkv, t0 = j / A.Hkv * TT;
+        if (j / A.Hkv != tile) {
+          tile = j / A.Hkv;
+          n = min(TT, A.tokens - t0);
+          __syncthreads();  // the tile before is done with its rows
+          resolve(A, t0, n, s_seq, s_pos, s_row);
+          mine = lane0 < n && s_row[lane0] >= 0;
+          if (kOnce && mine) P.turn(A.rope, p, s_pos[lane0], false);
+        }
+        T* key = s_key[(j - j0) & 1];
         auto put = [&](int i, Chunk<T, E> (&c)[4]) {
           if (P.turned) P.apply(c[0], c[1]);
           const size_t at = static_cast<size_t>(s_row[i] + h * A.ps) * D;
@@ -449,17 +461,15 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
           c[1].template put<(LD * sizeof(T)) % 16 == 0>(key + i * LD + P.b);
         };
         if constexpr (kOnce) {
-          if (mine) {
-            Chunk<T, E> c[4] = {next[0], next[1], next[2], next[3]};
-            if (h + 1 < h1) load(lane0, h + 1, next);
-            put(lane0, c);
-          }
+          Chunk<T, E> c[4] = {next[0], next[1], next[2], next[3]};
+          load_next(j + 1);
+          if (mine) put(lane0, c);
         } else {
           for (int i = lane0; i < n; i += LANES) {
             if (s_row[i] < 0) continue;
             P.turn(A.rope, p, s_pos[i], false);
             Chunk<T, E> c[4];
-            load(i, h, c);
+            load(t0 + i, h, c);
             put(i, c);
           }
         }
@@ -602,16 +612,19 @@ int run_append(AppendArgs& a, bool vec, int sms, cudaStream_t st) {
   a.tok_block = s.tok_block;
   a.row_y = s.row_y;
   a.key_blocks = 0;
-  a.key_heads = 1;
   if constexpr (PROXY != VATTN_EXACT) {
-    // as many heads per block as still leave four blocks for every SM
     const int TT = vec ? KeyTile<T, D, E, PROXY>::TT : KeyTile<T, D, 1, PROXY>::TT;
-    const long long tiles = (a.tokens + TT - 1) / TT;
-    const long long most = std::max(1LL, std::min<long long>(a.Hkv, tiles * a.Hkv / (4LL * sms)));
-    const int splits = static_cast<int>((a.Hkv + most - 1) / most);
-    a.key_heads = (a.Hkv + splits - 1) / splits;
-    const long long blocks = tiles * ((a.Hkv + a.key_heads - 1) / a.key_heads);
-    if (blocks > 0x3FFFFFFFLL) return VATTN_EINVAL;
+    const long long jobs = (static_cast<long long>(a.tokens) + TT - 1) / TT * a.Hkv;
+    if (jobs > 0x3FFFFFFFLL) return VATTN_EINVAL;
+    // three fit an SM. With queries behind them, which fill the SMs that they
+    // leave, blocks stay within a tile, with as many of its heads as still give
+    // every SM its three (8192 tokens, dim-major: 44 us; cut evenly 47.6)
+    long long blocks = std::min(jobs, 3LL * sms);
+    if (rows > 0) {
+      int heads = a.Hkv;
+      while (heads > 1 && (a.Hkv % heads || jobs / heads < 3LL * sms)) heads--;
+      blocks = jobs / heads;
+    }
     a.key_blocks = static_cast<int>(blocks);
   }
   const long long gx =
