@@ -77,7 +77,8 @@ class SparseDecoder:
         return out
 
     def _stream(self, stream):
-        return torch.cuda.current_stream(self.device) if stream is None else stream
+        # the context's device's current stream (the raw handle: no stream object is made per call)
+        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream
 
     def _check_cache(self, name, t, num_pages, shape, index):
         if t is None or t.dtype is not self.dtype or t.shape[1:] != shape or not t.is_contiguous():

@@ -43,26 +43,25 @@ class Rotary:
         rotate in place); new and contiguous by default. transpose: the transposed
         rotation, which turns the gradient of the result into that of x.
         """
-        if x.dim() != 3 or x.shape[2] != self.head_dim or x.stride(2) != 1:
-            raise ValueError(f"x must be [tokens, heads, {self.head_dim}] with contiguous components")
+        shape, strides, index = x.shape, x.stride(), x.get_device()
         dtype = _DTYPES.get(x.dtype)
-        if dtype is None:
-            raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
-        if not x.is_cuda:
-            raise ValueError("x must be on a CUDA device")
-        tokens, heads, _ = x.shape
+        if len(shape) != 3 or shape[2] != self.head_dim or strides[2] != 1 or dtype is None or index < 0:
+            raise ValueError(f"x must be float32 or bfloat16 [tokens, heads, {self.head_dim}] on a CUDA device, with "
+                             "contiguous components")
+        tokens, heads, _ = shape
         if positions.dtype is not torch.int32 or positions.shape != (tokens,) or not positions.is_contiguous() \
-                or positions.device != x.device:
+                or positions.get_device() != index:
             raise ValueError("positions must be contiguous int32 [tokens] on x's device")
         if out is None:
             out = torch.empty((tokens, heads, self.head_dim), dtype=x.dtype, device=x.device)
-        elif out.shape != x.shape or out.dtype is not x.dtype or out.device != x.device or out.stride(2) != 1:
+        elif out.shape != shape or out.dtype is not x.dtype or out.get_device() != index or out.stride(2) != 1:
             raise ValueError("out must be like x")
-        if x.device.index != torch.cuda.current_device():
-            with torch.cuda.device(x.device):
-                _abi.vattn_rotate(self.plan, x, out, positions, tokens, heads, dtype, x.stride()[:2],
-                                  out.stride()[:2], transpose, stream)
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(index)
+        args = (self.plan, x, out, positions, tokens, heads, dtype, strides[:2], out.stride()[:2], transpose, stream)
+        if index == torch.cuda.current_device():
+            _abi.vattn_rotate(*args)
         else:
-            _abi.vattn_rotate(self.plan, x, out, positions, tokens, heads, dtype, x.stride()[:2], out.stride()[:2],
-                              transpose, stream)
+            with torch.cuda.device(index):
+                _abi.vattn_rotate(*args)
         return out
