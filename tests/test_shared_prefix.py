@@ -111,6 +111,16 @@ def test_shared_many_rows(dtype, B, Hq, Hkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("groups,size,prefix", [(17, 2, 40), (40, 3, 150), (1, 400, 200), (1100, 1, 0), (700, 2, 33)])
+def test_shared_many_groups_and_sequences(dtype, groups, size, prefix):
+    # more groups or sequences than the kernels keep in shared memory
+    B = groups * size
+    _run([size] * groups, [max(prefix - g % 7, 0) for g in range(groups)], [(5 * b) % 23 for b in range(B)], dtype=dtype,
+         d=64, Hq=2, Hkv=1)
+
+
+@pytest.mark.gpu
 def test_shared_long_prefix():
     _run([6, 10], [20001, 9000], [(31 * b) % 300 for b in range(16)], Hq=16, Hkv=4)
 

@@ -42,11 +42,11 @@ struct PrefixTcShape {
   static constexpr int TILE = H * HALF;              // a Q, K or V tile
   static constexpr int NST = 160 * 1024 / TILE;      // ring tiles
   static constexpr int THREADS = 320;
-  static constexpr int GROUPS = 16;                  // groups whose records fit shared memory
+  static constexpr int GROUPS = 16;                  // groups whose records fit shared memory (below a warp)
   struct Tail {
     uint64_t full[NST], empty[NST], qfull, qfree, s[2], p[2][2], o[2], ofree, done;
     unsigned tmem;
-    int ok[GROUPS];
+    int start[GROUPS + 1], prefix[GROUPS], reach[GROUPS];
     SharedGroup group[GROUPS + 1];
     float2 ml[2][128];
   };
@@ -219,21 +219,59 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
-  grid_dependency_wait();
-  grid_dependents_launch();  // the next kernel takes each SM as this one leaves it (k_shared_own)
-  // the groups' records, all at once
+  // The groups' records. With few groups every CTA finds them itself, from what
+  // the caller gave, and starts while k_shared_prep runs (which lets this kernel
+  // start once everything before the call has ended): that takes its 4 us out of
+  // the way. It needs nothing else of k_shared_prep: for pages that are out of
+  // range it reads others, and k_shared_combine does not read the records.
   const bool cached = P.groups <= S::GROUPS;
   if (cached) {
-    constexpr int W = sizeof(SharedGroup) / 16;
-    for (int i = threadIdx.x; i < (P.groups + 1) * W; i += S::THREADS)
-      reinterpret_cast<uint4*>(tail.group)[i] = reinterpret_cast<const uint4*>(P.W.group)[i];
-    for (int i = threadIdx.x; i < P.groups; i += S::THREADS) tail.ok[i] = P.W.pages_ok[i];
+    const int mine = threadIdx.x < P.D.batch ? checked_len(P, threadIdx.x) : -1;
+    if (threadIdx.x <= P.groups) tail.start[threadIdx.x] = __ldcg(P.group_start + threadIdx.x);
+    if (threadIdx.x < P.groups) {
+      tail.prefix[threadIdx.x] = __ldcg(P.prefix_lens + threadIdx.x);
+      tail.reach[threadIdx.x] = 0;
+    }
+    __syncthreads();
+    bool bad = tail.start[0] != 0 || tail.start[P.groups] != P.D.batch;
+    for (int g = 0; g < P.groups; g++) bad |= tail.start[g + 1] < tail.start[g];
+    for (int b = threadIdx.x; b < P.D.batch && !bad; b += S::THREADS) {
+      const int n = b < S::THREADS ? mine : checked_len(P, b);
+      int g = 0;
+      while (tail.start[g + 1] <= b) g++;
+      const int prefix = tail.prefix[g];
+      if (prefix > 0 && prefix <= P.D.max_ctx && n >= prefix) atomicAdd(&tail.reach[g], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane g: group g; lane `groups`: the totals
+      SharedGroup r = {};
+      long long tiles = 0, rows = 0;
+      if (lane < P.groups) {
+        r.b0 = tail.start[lane];
+        r.size = tail.start[lane + 1] - r.b0;
+        r.prefix = tail.prefix[lane];
+        if (!bad && tail.reach[lane] >= 2) group_work(P, r, tiles, rows);
+      }
+      long long it = tiles, ir = rows;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, it, o), y = __shfl_up_sync(0xffffffffu, ir, o);
+        if (lane >= o) {
+          it += x;
+          ir += y;
+        }
+      }
+      r.tile0 = it - tiles;
+      r.row0 = ir - rows;
+      if (lane <= P.groups) tail.group[lane] = r;
+    }
+  } else {
+    grid_dependency_wait();
   }
   __syncthreads();
   tc_fence_after();
   const unsigned tmem = tail.tmem;
   const SharedGroup* group = cached ? tail.group : P.W.group;
-  const int* pages_ok = cached ? tail.ok : P.W.pages_ok;
   const long long Tt = group[P.groups].tile0;
   const long long beg = div_nonneg(Tt * blockIdx.x, gridDim.x), end = div_nonneg(Tt * (blockIdx.x + 1), gridDim.x);
   int gi = group_at(P, group, beg);
@@ -245,11 +283,16 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
     const int blk = lane / H, hf = lane % H;
     unsigned li = 0;
     int seg = 0;
+    // With the first ring full: wait for k_shared_prep, then let k_shared_own
+    // start, which takes each SM as this kernel leaves it.
+    auto release = [&]() {
+      grid_dependency_wait();
+      grid_dependents_launch();
+    };
     for (long long cur = beg; cur < end && ok;) {
       const Segment s = segment_at(P, group, cur, end, gi);
       gi = s.gi;
       cur = s.next;
-      if (!pages_ok[s.gi]) continue;
       const int tiles_q = s.rows > 128 ? 2 : 1;
       // first row of this lane's block of key tile t (-1: behind the prefix)
       const int* pages = P.D.page_table + static_cast<size_t>(s.b0) * P.D.pps;
@@ -257,7 +300,9 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
         const int pos = t * KT + blk * box;
         if (t >= s.t1 || lane >= per || pos >= s.prefix) return -1;
         const int slot = page_slot(P.D, pos);
-        return (pages[slot] * P.D.Hkv + s.h) * P.D.ps + (pos - slot * P.D.ps);
+        int page = __ldcg(pages + slot);
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(P.D.num_pages)) page = 0;  // reported by k_shared_prep
+        return (page * P.D.Hkv + s.h) * P.D.ps + (pos - slot * P.D.ps);
       };
       int row = row_of(s.t0);
       for (int t = s.t0; t < s.t1 && ok; t++) {
@@ -265,6 +310,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
         const int nblk = min(KT / box, (s.prefix - t * KT + box - 1) / box);
         for (int kv = 0; kv < 2; kv++, li++) {
           const unsigned st = li % NST;
+          if (li == NST) release();
           if (li >= NST) ok = __all_sync(0xffffffffu, mbar_wait(&tail.empty[st], (li / NST - 1) & 1u));
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&tail.full[st], static_cast<unsigned>(nblk * box * D * 2));
@@ -288,6 +334,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
         }
       }
     }
+    if (li <= NST) release();
     // no copy may land after the CTA has moved on (only after a failed wait are some still in flight)
     if (!ok) {
       for (unsigned i = li > NST ? li - NST : 0; i < li; i++) mbar_wait(&tail.full[i % NST], (i / NST) & 1u);
@@ -305,8 +352,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
         const Segment s = segment_at(P, group, cur, end, gi);
         gi = s.gi;
         cur = s.next;
-        if (!pages_ok[s.gi]) continue;
-        const bool two = s.rows > 128;
+          const bool two = s.rows > 128;
         const int nt = s.t1 - s.t0, n = two ? 2 * nt : nt;
         auto qk = [&](int i) {
           const int st = i & 1, kt = two ? i >> 1 : i;
@@ -377,18 +423,24 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       const Segment s = segment_at(P, group, cur, end, gi);
       gi = s.gi;
       cur = s.next;
-      if (!pages_ok[s.gi]) continue;
       const bool two = s.rows > 128;
       const int nt = s.t1 - s.t0, steps = two ? nt : (nt + 1 - st) / 2;
       const int valid = two ? s.rows - st * 128 : s.rows;  // query rows of the stage's tile
       const bool idle = quarter * 32 >= valid;             // none in this warp
       float m = -INFINITY, l = 0.0f;
-      for (int i = 0; i < steps && ok; i++) {
+      // Before its first scores can be there, a warp runs a step on whatever its
+      // TMEM holds, without storing, waiting or signalling: the instructions are
+      // then in the SM's cache when the scores arrive (they are several KB, and
+      // came from L2 at the first tile's expense).
+      for (int i = ns == 0 ? -1 : 0; i < steps && ok; i++) {
+        const bool real = i >= 0;
         const int kt = two ? i : 2 * i + st;
-        const int nk = s.prefix - (s.t0 + kt) * KT;
-        ok = __all_sync(0xffffffffu, mbar_wait(&tail.s[st], ns & 1u));
-        ns++;
-        if (!ok) break;
+        const int nk = real ? s.prefix - (s.t0 + kt) * KT : KT;
+        if (real) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&tail.s[st], ns & 1u));
+          ns++;
+          if (!ok) break;
+        }
         if (nk < KT && (!two || st == 0)) {
           // the V rows behind the prefix's last key: zero, whatever the cache holds.
           // (The tile's scores are there, so every earlier use of V's ring tile is
@@ -419,7 +471,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
             top = fmaxf(top, max64(x));
           }
           top *= c;
-          if (i == 0) {
+          if (i <= 0) {
             m = fmaxf(top, -1e30f);  // finite: scores of -inf weigh exactly 0
           } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
             const float mn = top > m + kRescale ? top : m;
@@ -460,16 +512,16 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
                 const float2 d = __fadd2_rn(p, make_float2(-h.x, -h.y));
                 w[16 + j] = pack_bf16x2(d.x, d.y);
               }
-              tc_st32(sa + 64 * half + 32 * k, w);
+              if (real) tc_st32(sa + 64 * half + 32 * k, w);
               if (half == 0) tc_ld32(sa + 64 + 32 * k, x[k]);
             }
             tc_wait_st();
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tail.p[st][half]);
+          if (real && lane == 0) mbar_arrive(&tail.p[st][half]);
         }
-        l += sum.x + sum.y;
+        l = i <= 0 ? sum.x + sum.y : l + (sum.x + sum.y);
       }
       li0 += 2u * nt;
       if (!ok) break;
@@ -489,10 +541,10 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       }
       const bool has = two || merge || st == 0;  // columns to write
       const int s0 = two ? st : 0;               // the (first) accumulator
-      if (two || merge || st == 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&tail.o[s0], no[s0] & 1u));
-        if (merge && ok) ok = __all_sync(0xffffffffu, mbar_wait(&tail.o[1], no[1] & 1u));
-      }
+      // (a stage without a step waits too: it would run ahead otherwise, and
+      // arrive at `ofree` for segments whose accumulators are still being read)
+      ok = __all_sync(0xffffffffu, mbar_wait(&tail.o[s0], no[s0] & 1u));
+      if (merge && ok) ok = __all_sync(0xffffffffu, mbar_wait(&tail.o[1], no[1] & 1u));
       no[0]++;
       if (two || merge) no[1]++;
       if (!ok) break;

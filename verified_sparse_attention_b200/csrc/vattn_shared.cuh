@@ -51,6 +51,14 @@ __device__ __forceinline__ long long block_row0(const SharedParams& P, int mb, i
   return static_cast<long long>(mb) * P.RB * P.D.Hkv + static_cast<long long>(h) * rows;
 }
 
+// Key tiles and record rows of a shared group (its sequences and prefix given).
+__device__ __forceinline__ void group_work(const SharedParams& P, SharedGroup& g, long long& tiles, long long& rows) {
+  const int nrow = g.size * P.D.G;
+  g.tiles = (g.prefix + P.KT - 1) / P.KT;
+  tiles = static_cast<long long>(g.tiles) * ((nrow + P.RB - 1) / P.RB) * P.D.Hkv;
+  rows = static_cast<long long>(nrow) * P.D.Hkv;
+}
+
 // Chunks of k_shared_own that cover positions [start, n): kOwnChunk positions
 // each from the 16-position block that holds `start`. Warps take them in pieces
 // of at least kOwnPiece chunks of one (sequence, KV head), about kOwnPieces a
@@ -66,7 +74,7 @@ constexpr int kSharedPrepThreads = 256;
 constexpr int kSharedPrepKeep = 1024;  // sequences and groups kept in shared memory by the last CTA
 
 __device__ __forceinline__ int checked_len(const SharedParams& P, int b) {
-  const int n = P.D.seq_lens[b];
+  const int n = __ldcg(P.D.seq_lens + b);
   return n < 0 || n > P.D.max_ctx ? -1 : n;
 }
 
@@ -117,8 +125,10 @@ __device__ __forceinline__ long long block_scan_ll(long long v, long long* s_w) 
 static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const __grid_constant__ SharedParams P) {
   const int tid = threadIdx.x, cta = blockIdx.x;
   const DevParams& D = P.D;
-  grid_dependents_launch();
+  // (the tensor-core prefix kernel starts on this signal, before this kernel's
+  // end: everything before the call has to have ended)
   grid_dependency_wait();
+  grid_dependents_launch();
 
   if (cta < D.batch + P.groups) {
     __shared__ int s_g, s_bad;
@@ -243,12 +253,7 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
         rec.b0 = start_of(g);
         rec.size = start_of(g + 1) - rec.b0;
         rec.prefix = prefix_of(g);
-        if (reach_of(g) >= 2) {
-          const int nrow = rec.size * D.G;
-          rec.tiles = (rec.prefix + P.KT - 1) / P.KT;
-          t = static_cast<long long>(rec.tiles) * ((nrow + P.RB - 1) / P.RB) * D.Hkv;
-          r = static_cast<long long>(nrow) * D.Hkv;
-        }
+        if (reach_of(g) >= 2) group_work(P, rec, t, r);
       }
       const long long it = block_scan_ll(t, s_w), ir = block_scan_ll(r, s_w);
       if (g < P.groups) {
