@@ -21,6 +21,7 @@
 //                   tensor core, so every cycle between two products of this
 //                   thread idles it: no warp-wide step stands there, and the
 //                   weights are handed over in two halves of 64 keys
+//   warp 10         lets the next kernel start
 // TMEM (512 columns): S0, S1, O0, O1 of 128 each. The weights of 32 keys
 // overwrite their scores as two bf16 terms (hi = bf16(p), lo = bf16(p - hi),
 // 2^-17 relative; 16 columns each), the A operand of two products with V: fp32 outputs keep fp32's accuracy from
@@ -41,7 +42,7 @@ struct PrefixTcShape {
   static constexpr int HALF = 128 * 128;             // bytes of 128 rows of a 64-column half
   static constexpr int TILE = H * HALF;              // a Q, K or V tile
   static constexpr int NST = 160 * 1024 / TILE;      // ring tiles
-  static constexpr int THREADS = 320;
+  static constexpr int THREADS = 352;
   static constexpr int GROUPS = 16;                  // groups whose records fit shared memory (below a warp)
   struct Tail {
     uint64_t full[NST], empty[NST], qfull, qfree, s[2], p[2][2], o[2], ofree, done;
@@ -283,12 +284,6 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
     const int blk = lane / H, hf = lane % H;
     unsigned li = 0;
     int seg = 0;
-    // With the first ring full: wait for k_shared_prep, then let k_shared_own
-    // start, which takes each SM as this kernel leaves it.
-    auto release = [&]() {
-      grid_dependency_wait();
-      grid_dependents_launch();
-    };
     for (long long cur = beg; cur < end && ok;) {
       const Segment s = segment_at(P, group, cur, end, gi);
       gi = s.gi;
@@ -310,7 +305,6 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
         const int nblk = min(KT / box, (s.prefix - t * KT + box - 1) / box);
         for (int kv = 0; kv < 2; kv++, li++) {
           const unsigned st = li % NST;
-          if (li == NST) release();
           if (li >= NST) ok = __all_sync(0xffffffffu, mbar_wait(&tail.empty[st], (li / NST - 1) & 1u));
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&tail.full[st], static_cast<unsigned>(nblk * box * D * 2));
@@ -334,7 +328,6 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
         }
       }
     }
-    if (li <= NST) release();
     // no copy may land after the CTA has moved on (only after a failed wait are some still in flight)
     if (!ok) {
       for (unsigned i = li > NST ? li - NST : 0; i < li; i++) mbar_wait(&tail.full[i % NST], (i / NST) & 1u);
@@ -411,6 +404,11 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       if (!ok) atomicOr(P.D.err, kDevTimeout);
     }
     __syncwarp();
+  } else if (warp == 10) {
+    // k_shared_own may start once k_shared_prep has ended; it takes each SM as
+    // this kernel leaves it
+    grid_dependency_wait();
+    grid_dependents_launch();
   } else {
     // ------------------------------------------------------------ softmax
     const int st = warp >> 2, quarter = warp & 3;
@@ -574,7 +572,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       if (lane == 0) mbar_arrive(&tail.ofree);
     }
   }
-  if (!ok && lane == 0 && warp != 9) atomicOr(P.D.err, kDevTimeout);
+  if (!ok && lane == 0 && warp < 9) atomicOr(P.D.err, kDevTimeout);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

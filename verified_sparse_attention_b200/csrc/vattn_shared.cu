@@ -198,16 +198,18 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
       return ctx->last_status = rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int launches = 0;
-  vattn::launch(vattn::k_shared_prep, dim3(batch + groups + 2), dim3(vattn::kSharedPrepThreads), 0, st, P, &launches);
+  const int prep_warps = vattn::kSharedPrepThreads / 32;
+  vattn::launch(vattn::k_shared_prep, dim3((batch + groups + prep_warps - 1) / prep_warps + 2),
+                dim3(vattn::kSharedPrepThreads), 0, st, P, &launches);
   vattn::launch(k.prefix, dim3(ctx->num_sms), dim3(k.threads), k.smem, st, P, &launches);
   if (k.own)
     vattn::launch(k.own, dim3(ctx->num_sms), dim3(k.own_nw * 32), k.own_smem, st, P, &launches);
   else
     vattn::launch(k.gather, dim3(ctx->gather_grid), dim3(k.gather_threads), k.gather_smem, st, P.D, &launches);
-  // as many warps per row as may be resident together (64 per SM)
+  // as many warps per row as keep within 32 warps per SM (64: 3 to 4 us more)
   const int rows = batch * c.num_q_heads;
   int w = 3;
-  while (w > 0 && (rows << w) > 64 * ctx->num_sms) w--;
+  while (w > 0 && (rows << w) > 32 * ctx->num_sms) w--;
   const int per = vattn::kSharedCombWarps >> w;
   vattn::launch(k.combine[w], dim3((rows + per - 1) / per), dim3(vattn::kSharedCombWarps * 32), 0, st, P, &launches);
   return vattn::finish(ctx, launches);

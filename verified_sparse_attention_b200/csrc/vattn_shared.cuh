@@ -78,29 +78,29 @@ __device__ __forceinline__ int checked_len(const SharedParams& P, int b) {
   return n < 0 || n > P.D.max_ctx ? -1 : n;
 }
 
-// Whether any of the page ids of row `b` in slots [s0, s1) is out of range.
-__device__ __forceinline__ int bad_pages(const SharedParams& P, int b, int s0, int s1) {
+// Whether any of the page ids of row `b` in slots [s0, s1) is out of range (a warp).
+__device__ __forceinline__ bool bad_pages(const SharedParams& P, int b, int s0, int s1) {
   int bad = 0;
-  for (int i0 = s0 + threadIdx.x; i0 < s1; i0 += 8 * blockDim.x) {  // eight independent loads in flight
+  for (int i0 = s0 + (threadIdx.x & 31); i0 < s1; i0 += 8 * 32) {  // eight independent loads in flight
     int pid[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const int i = i0 + j * blockDim.x;
+      const int i = i0 + j * 32;
       pid[j] = i < s1 ? P.D.page_table[static_cast<size_t>(b) * P.D.pps + i] : 0;
     }
 #pragma unroll
     for (int j = 0; j < 8; j++)
       if (pid[j] < 0 || pid[j] >= P.D.num_pages) bad = 1;
   }
-  return __syncthreads_or(bad);
+  return __any_sync(0xffffffffu, bad);
 }
 
-// Sequences of [b0, b1) that reach position `prefix` (the whole block).
+// Sequences of [b0, b1) that reach position `prefix` (a warp).
 __device__ __forceinline__ int count_reach(const SharedParams& P, int b0, int b1, int prefix) {
   int cnt = 0;
-  for (int base = b0; base < b1; base += blockDim.x) {
-    const int b = base + threadIdx.x;
-    cnt += __syncthreads_count(b < b1 && prefix > 0 && checked_len(P, b) >= prefix);
+  for (int base = b0; base < b1; base += 32) {
+    const int b = base + (threadIdx.x & 31);
+    cnt += __popc(__ballot_sync(0xffffffffu, b < b1 && prefix > 0 && checked_len(P, b) >= prefix));
   }
   return cnt;
 }
@@ -120,36 +120,36 @@ __device__ __forceinline__ long long block_scan_ll(long long v, long long* s_w) 
   return v;
 }
 
-// CTA b < batch: sequence b; CTA batch + g: group g (its pages); the last two
-// CTAs: the prefix kernel's work and the own parts' as prefix sums.
+// The last two CTAs find the prefix kernel's work and the own parts' as prefix
+// sums; every warp of the others one sequence or one group (its pages). Few
+// CTAs, because the prefix kernel, which runs beside them, has to wait for the
+// SMs that they are on.
 static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const __grid_constant__ SharedParams P) {
-  const int tid = threadIdx.x, cta = blockIdx.x;
+  const int tid = threadIdx.x;
   const DevParams& D = P.D;
   // (the tensor-core prefix kernel starts on this signal, before this kernel's
   // end: everything before the call has to have ended)
   grid_dependency_wait();
   grid_dependents_launch();
 
-  if (cta < D.batch + P.groups) {
-    __shared__ int s_g, s_bad;
-    if (tid == 0) {
-      s_g = -1;
-      s_bad = 0;
-    }
-    __syncthreads();
+  if (blockIdx.x < gridDim.x - 2) {
+    const int job = blockIdx.x * (kSharedPrepThreads / 32) + (tid >> 5), lane = tid & 31;
+    if (job >= D.batch + P.groups) return;
     // the bounds ascend from 0 to batch, or nothing is decoded; with ascending
     // bounds at most one group holds a sequence
-    for (int g = tid; g < P.groups; g += blockDim.x) {
+    int bad = 0, own = -1;
+    for (int g = lane; g < P.groups; g += 32) {
       const int lo = P.group_start[g], hi = P.group_start[g + 1];
-      if (hi < lo || (g == 0 && lo != 0) || (g == P.groups - 1 && hi != D.batch)) s_bad = 1;
-      if (cta < D.batch && lo <= cta && cta < hi) s_g = g;
+      if (hi < lo || (g == 0 && lo != 0) || (g == P.groups - 1 && hi != D.batch)) bad = 1;
+      if (job < D.batch && lo <= job && job < hi) own = g;
     }
-    __syncthreads();
-    const bool bad_bounds = s_bad != 0;
-    if (cta < D.batch) {
-      const int b = cta, g = s_g;
+    const bool bad_bounds = __any_sync(0xffffffffu, bad);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) own = max(own, __shfl_xor_sync(0xffffffffu, own, o));
+    if (job < D.batch) {
+      const int b = job, g = own;
       int n = checked_len(P, b), start = 0;
-      if (tid == 0 && n < 0) atomicOr(D.err, kDevBadSeqlen);
+      if (lane == 0 && n < 0) atomicOr(D.err, kDevBadSeqlen);
       if (n < 0 || bad_bounds || g < 0) n = 0;
       if (n > 0) {
         const int prefix = P.prefix_lens[g];
@@ -161,10 +161,10 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
       }
       // only the positions behind the prefix are read through this row
       if (n > start && bad_pages(P, b, start / D.ps, (n + D.ps - 1) / D.ps)) {
-        if (tid == 0) atomicOr(D.err, kDevBadPage);
+        if (lane == 0) atomicOr(D.err, kDevBadPage);
         n = 0;
       }
-      for (int h = tid; h < D.Hkv; h += blockDim.x) {
+      for (int h = lane; h < D.Hkv; h += 32) {
         UnitInfo inf = {};
         inf.n = n;
         inf.s1 = start;
@@ -173,27 +173,27 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
       }
       return;
     }
-    const int g = cta - D.batch;
+    const int g = job - D.batch;
     int ok = 0;
     if (!bad_bounds) {
       const int prefix = P.prefix_lens[g], b0 = P.group_start[g], b1 = P.group_start[g + 1];
       if (prefix < 0 || prefix > D.max_ctx) {
-        if (tid == 0) atomicOr(D.err, kDevBadGroup);
+        if (lane == 0) atomicOr(D.err, kDevBadGroup);
       } else {
         ok = 1;
         if (count_reach(P, b0, b1, prefix) >= 2 && bad_pages(P, b0, 0, (prefix + D.ps - 1) / D.ps)) {
-          if (tid == 0) atomicOr(D.err, kDevBadPage);
+          if (lane == 0) atomicOr(D.err, kDevBadPage);
           ok = 0;
         }
       }
     }
-    if (tid == 0) P.W.pages_ok[g] = ok;
+    if (lane == 0) P.W.pages_ok[g] = ok;
     return;
   }
 
   // ---- prefix sums. The inputs come into shared memory in one round of loads
   // (what does not fit is read where it is).
-  const bool own_cta = cta == D.batch + P.groups + 1;
+  const bool own_cta = blockIdx.x == gridDim.x - 1;
   int* g_reach = P.W.reach + (own_cta ? P.groups : 0);
   __shared__ int s_len[kSharedPrepKeep], s_prefix[kSharedPrepKeep], s_reach[kSharedPrepKeep];
   __shared__ int s_start[kSharedPrepKeep + 1];
@@ -630,6 +630,10 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
   if (lane < NS) mbar_init(&bars[lane], 1);
   mbar_init_fence();
   __syncwarp();
+  grid_dependents_launch();  // k_shared_combine fills the SMs that this kernel leaves
+  // (the array holds more entries than there are warps, used or not)
+  const int4* first = reinterpret_cast<const int4*>(&P.W.own_piece[gw / Q.Hkv]);
+  const int4 first_a = __ldcg(first), first_b = __ldcg(first + 1);
   const int total = __ldcg(&P.W.own_pre[Q.batch]) * Q.Hkv;
   const float c = Q.scale * 1.4426950408889634f;  // scores in log2 units
 
@@ -639,12 +643,21 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
     // steps, one with every chunk copied: its index, its entry, its state and
     // first page.
     OwnPiece pp, pn;
-    int px = 0, page = 0, id_n = gw, page_n = 0, n_n = 0, step = 1;
+    int px = 0, page = 0, id_n = gw, page_n = 0, n_n = 0, step = 2;
     unsigned nq = 0, dq = 0;  // pieces queued and taken
     unsigned ni = 0, nc = 0;  // chunks copied and computed (stage and phase follow)
     auto page_of = [&](const OwnPiece& p, int x) -> int {
       return __ldcg(Q.page_table + static_cast<size_t>(p.b) * Q.pps + page_slot(Q, p.pos + kOwnChunk * x));
     };
+    auto take = [&](const int4& a, const int4& b) {
+      pn.b = a.x;
+      pn.pos = a.y;
+      pn.chunks = a.z;
+      pn.start = a.w;
+      pn.n = b.x;
+      pn.id = id_n;
+    };
+    take(first_a, first_b);
     auto fetch_step = [&]() {  // 0 -> 3; 4: no piece is left
       if (step == 0) {
         if (lane == 0) id_n = W + atomicAdd(&P.W.own_next[0], 1);
@@ -654,13 +667,7 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
         step = id_n < total ? 2 : 4;
         if (step == 2) {
           const int4* e = reinterpret_cast<const int4*>(&P.W.own_piece[id_n / Q.Hkv]);
-          const int4 a = __ldcg(e), b = __ldcg(e + 1);
-          pn.b = a.x;
-          pn.pos = a.y;
-          pn.chunks = a.z;
-          pn.start = a.w;
-          pn.n = b.x;
-          pn.id = id_n;
+          take(__ldcg(e), __ldcg(e + 1));
         }
       } else if (step == 2) {
         n_n = __ldcg(&Q.info[static_cast<size_t>(pn.b) * Q.Hkv].n);
@@ -836,7 +843,6 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
       for (; nc != ni; nc++) mbar_wait(&bars[nc % NS], (nc / NS) & 1u);  // no copy lands after the warp has moved on
     }
   }
-  grid_dependents_launch();
   grid_dependency_wait();
 }
 
@@ -855,19 +861,24 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const DevParams& Q = P.D;
   const int row_out = blockIdx.x * (kSharedCombWarps / WR) + warp / WR, part = warp % WR;
-  grid_dependency_wait();
+  // With k_shared_own before it the kernel starts after k_shared_prep's end, and
+  // finds where its records are while the last of them are written; what
+  // k_shared_prep wrote is read past L1. Behind the gather it waits first.
+  if (!P.own_warps) grid_dependency_wait();
+  grid_dependents_launch();
   const bool real = row_out < Q.batch * Q.Hq;
   const int b = real ? row_out / Q.Hq : 0, hq = row_out % Q.Hq, h = hq / Q.G, gh = hq % Q.G, u = b * Q.Hkv + h;
-  const UnitInfo inf = Q.info[u];
+  const int4 i0 = __ldcg(reinterpret_cast<const int4*>(Q.info + u));  // n, s1, wst, k
+  const int n_pos = i0.x, start = i0.y, gi = i0.w;
   float2* out = reinterpret_cast<float2*>(Q.out + static_cast<size_t>(row_out) * D);
-  const bool shared = inf.s1 > 0;
-  const bool none = inf.n <= 0 || (shared && !P.W.pages_ok[inf.k]);
+  const bool shared = start > 0;
+  const bool none = n_pos <= 0 || (shared && !__ldcg(P.W.pages_ok + gi));
   // records of the own part
   long long To = 0, own0 = 0;
   SliceRecs own{0, 0, 0, false};
   if (P.own_warps) {
-    own0 = P.W.own_pre[b];
-    own.n = P.W.own_pre[b + 1] - static_cast<int>(own0);
+    own0 = __ldcg(P.W.own_pre + b);
+    own.n = __ldcg(P.W.own_pre + b + 1) - static_cast<int>(own0);
   } else {
     To = Q.pre_det[2 * Q.units];
     own = slice_recs(Q.pre_det, 2 * u, To, Q.CD);
@@ -877,8 +888,11 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
   long long Tp = 0, base = 0;
   const int C = P.W.grid;
   if (shared) {
-    const SharedGroup g = P.W.group[inf.k];
-    Tp = P.W.group[P.groups].tile0;
+    SharedGroup g;
+    const int4* gp = reinterpret_cast<const int4*>(P.W.group + gi);
+    reinterpret_cast<int4*>(&g)[0] = __ldcg(gp);
+    reinterpret_cast<int4*>(&g)[1] = __ldcg(gp + 1);
+    Tp = __ldcg(&P.W.group[P.groups].tile0);
     const int row = (b - g.b0) * Q.G + gh, mb = row / P.RB;
     const int rows = min(P.RB, g.size * Q.G - mb * P.RB);
     base = g.row0 + block_row0(P, mb, h, rows) + (row - mb * P.RB);
@@ -888,6 +902,7 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
     pre.n = pre.per_item ? g.tiles : cta_of(pre.x0 + g.tiles - 1, Tp, C) - pre.cf + 1;
   }
   const int np = pre.n, N = real && !none ? np + own.n : 0;
+  if (P.own_warps) grid_dependency_wait();
   float m = -INFINITY, l = 0.0f;
   float2 a[PL];
 #pragma unroll
