@@ -45,7 +45,7 @@ struct PrefixTcShape {
   static constexpr int THREADS = 352;
   static constexpr int GROUPS = 16;                  // groups whose records fit shared memory (below a warp)
   struct Tail {
-    uint64_t full[NST], empty[NST], qfull, qfree, s[2], p[2][2], o[2], ofree, done;
+    uint64_t full[NST], empty[NST], qfull, qfree, s[2], p[2][2], o[2], ofree, done, all;
     unsigned tmem;
     int start[GROUPS + 1], prefix[GROUPS], reach[GROUPS];
     SharedGroup group[GROUPS + 1];
@@ -182,6 +182,16 @@ __device__ __forceinline__ float max64(const unsigned (&x)[2][32]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
+// A barrier of several warps with a bounded wait: false if it ran out. `phase`
+// counts the warp's passes.
+__device__ __forceinline__ bool meet(uint64_t* bar, unsigned& phase) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1u));
+  phase++;
+  return ok;
+}
+
 constexpr float kRescale = 8.0f;  // log2 of the weights' bound before the maximum moves
 
 template <int D>
@@ -203,6 +213,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
     mbar_init(&tail.qfull, 1);
     mbar_init(&tail.qfree, 1);
     mbar_init(&tail.ofree, 8);
+    mbar_init(&tail.all, 8);
     mbar_init(&tail.done, 1);
     for (int i = 0; i < 2; i++) {
       mbar_init(&tail.s[i], 1);
@@ -416,7 +427,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
     const unsigned sa = tmem + st * 128 + lanes, oa = tmem + 256 + lanes;
     const float c = P.D.scale * 1.4426950408889634f;  // scores in log2 units
     const int r = quarter * 32 + lane;                // row of the query tile
-    unsigned ns = 0, no[2] = {0, 0}, li0 = 0;
+    unsigned ns = 0, no[2] = {0, 0}, li0 = 0, alls = 0;
     for (long long cur = beg; cur < end && ok;) {
       const Segment s = segment_at(P, group, cur, end, gi);
       gi = s.gi;
@@ -529,13 +540,14 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       float f0 = 1.0f, f1 = 0.0f;
       if (merge) {
         tail.ml[st][r] = make_float2(m, l);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        ok = meet(&tail.all, alls);
         const float2 a = tail.ml[0][r], b = tail.ml[1][r];
         m = fmaxf(a.x, b.x);
         f0 = ex2(a.x - m);
         f1 = ex2(b.x - m);
         l = a.y * f0 + b.y * f1;
-        asm volatile("bar.sync 1, 256;" ::: "memory");  // before the next segment's write
+        ok = meet(&tail.all, alls) && ok;  // before the next segment's write
+        if (!ok) break;
       }
       const bool has = two || merge || st == 0;  // columns to write
       const int s0 = two ? st : 0;               // the (first) accumulator
