@@ -332,6 +332,7 @@ int vattn_append(vattn_ctx* ctx, const vattn_append_params* params, const int32_
 /* ------------------------------------------------------------------------
  * Dense decode for a batch that shares prefixes: vattn_dense_decode's result,
  * with every shared prefix's keys and values read once per group of sequences.
+ *   groups       at least 1, at most max_batch
  *   group_start  [groups + 1] device int32, ascending from 0 to batch: group g
  *                is sequences group_start[g] .. group_start[g + 1] - 1
  *   prefix_lens  [groups] device int32, in [0, max_ctx]: positions

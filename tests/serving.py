@@ -78,6 +78,8 @@ def shared_batch(sizes, prefixes, own, *, Hq, Hkv, d, ps, dtype, seed=0, spare=2
     n_pages = 0
     content = []  # (page, rows written, copied from page)
     for k in range(len(sizes)):
+        if sizes[k] == 0:
+            continue
         whole, rest = divmod(prefixes[k], ps)
         first = start[k]
         shared = list(range(n_pages, n_pages + whole))

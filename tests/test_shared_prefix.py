@@ -52,10 +52,10 @@ def _tol(x, d):
     return 2 * (score + 2**-21 + 2**-17 + 2**-16) * float(torch.nan_to_num(x["v_cache"].float()).abs().max())
 
 
-def _decoder(x, dtype, ps, **kw):
+def _decoder(x, dtype, ps, max_batch=None, **kw):
     B, Hq, d = x["q"].shape
     return SparseDecoder(num_q_heads=Hq, num_kv_heads=x["k_cache"].shape[1], head_dim=d, dtype=DT[dtype], page_size=ps,
-                         max_batch=kw.pop("max_batch", B), max_ctx=x["max_ctx"], **kw)
+                         max_batch=max_batch or max(B, len(x["prefix_lens"])), max_ctx=x["max_ctx"], **kw)
 
 
 def _cuda(x):
@@ -118,6 +118,12 @@ def test_shared_many_groups_and_sequences(dtype, groups, size, prefix):
     B = groups * size
     _run([size] * groups, [max(prefix - g % 7, 0) for g in range(groups)], [(5 * b) % 23 for b in range(B)], dtype=dtype,
          d=64, Hq=2, Hkv=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_empty_groups(dtype):
+    _run([0, 3, 0, 0, 2, 0], [40, 100, 0, 7, 64, 1], [1, 5, 0, 20, 33], dtype=dtype, d=64)
 
 
 @pytest.mark.gpu
@@ -200,7 +206,7 @@ def test_shared_refusals_before_any_launch():
         return _abi.vattn_shared_dense_decode(dec.ctx, *a.values(), check=False)
 
     for bad in (dict(q=None), dict(k_cache=None), dict(page_table=None), dict(group_start=None),
-                dict(prefix_lens=None), dict(out=None), dict(groups=0), dict(groups=3), dict(batch=-1), dict(batch=3),
+                dict(prefix_lens=None), dict(out=None), dict(groups=0), dict(groups=-1), dict(batch=-1), dict(batch=3),
                 dict(num_pages=0), dict(q=y["q"].data_ptr() + 2), dict(k_cache=y["k_cache"].data_ptr() + 8)):
         assert rc(**bad) == _abi.VATTN_EINVAL, bad
     assert rc(batch=0, groups=0, q=None) == _abi.VATTN_OK

@@ -157,7 +157,7 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
   if (!ctx) return VATTN_EINVAL;
   ctx->last_status = VATTN_EINVAL;
   const vattn_config& c = ctx->cfg;
-  if (batch < 0 || batch > c.max_batch || groups < 0 || groups > batch || num_pages < 1) return VATTN_EINVAL;
+  if (batch < 0 || batch > c.max_batch || groups < 0 || groups > c.max_batch || num_pages < 1) return VATTN_EINVAL;
   if (batch > 0 && groups == 0) return VATTN_EINVAL;
   if (batch == 0) {
     ctx->last_launches = 0;
