@@ -50,7 +50,7 @@ def dense64(q, k_cache, v_cache, page_table, seq_lens):
     """Softmax attention of one token per sequence through its own page table, float64 [B, Hq, d]."""
     B, Hq, d = q.shape
     Hkv, ps = k_cache.shape[1], k_cache.shape[2]
-    out = torch.zeros(B, Hq, d, dtype=torch.float64)
+    out = torch.zeros(B, Hq, d, dtype=torch.float64, device=q.device)
     for b in range(B):
         n = int(seq_lens[b])
         if n == 0:

@@ -127,6 +127,35 @@ def test_shared_empty_groups(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,heads,prefix", [(3, 10, 70000), (140, 16, 24000), (2, 1, 130001)])
+def test_shared_prefix_of_many_tiles(B, heads, prefix):
+    # more key tiles in a row than one accumulator takes, one and two query tiles
+    g = torch.Generator(device="cuda").manual_seed(5)
+    d, ps = 64, 1024
+    whole, own = prefix // ps, 3 + prefix % ps
+    pages = whole + B
+    k, v = (torch.randn(pages, heads, ps * 2, d, generator=g, device="cuda").bfloat16()[:, :, :ps].contiguous()
+            for _ in range(2))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.cat([torch.arange(whole, **i32).expand(B, whole), whole + torch.arange(B, **i32)[:, None]], 1).contiguous()
+    # the page in which the prefix ends holds the same rows in every sequence
+    for c in (k, v):
+        c[whole + 1:, :, :prefix % ps] = c[whole, :, :prefix % ps].clone()
+    x = dict(q=torch.randn(B, heads, d, generator=g, device="cuda").bfloat16(), k_cache=k, v_cache=v, page_table=table,
+             seq_lens=torch.full((B,), whole * ps + own, **i32), group_start=torch.tensor([0, B], **i32),
+             prefix_lens=torch.tensor([prefix], **i32), num_pages=pages, max_ctx=(whole + 1) * ps)
+    # scores that rise along the prefix move the maximum behind the first accumulators
+    grow = torch.linspace(0.5, 2.0, whole, device="cuda")[:, None, None, None]
+    k[:whole] = (k[:whole].float() * grow).bfloat16()
+    dec = _decoder(x, "bf16", ps)
+    got = _call(dec, x).double()
+    assert dec.last_error() == 0
+    ref = dense64(x["q"], k, v, table, x["seq_lens"])
+    assert float((got - ref).abs().max()) <= 2 * _tol(x, d)    # keys of twice the size
+    dec.close()
+
+
+@pytest.mark.gpu
 def test_shared_long_prefix():
     _run([6, 10], [20001, 9000], [(31 * b) % 300 for b in range(16)], Hq=16, Hkv=4)
 

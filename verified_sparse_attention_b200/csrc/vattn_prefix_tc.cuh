@@ -182,6 +182,25 @@ __device__ __forceinline__ float max64(const unsigned (&x)[2][32]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
+// 16 columns of a record: scaled; plus an accumulator's (or just these).
+__device__ __forceinline__ void scale_record(float* p, float f) {
+  float4* q = reinterpret_cast<float4*>(p);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    float4 x = q[j];
+    q[j] = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+  }
+}
+__device__ __forceinline__ void add_record(float* p, const unsigned (&o)[16], bool more) {
+  float4* q = reinterpret_cast<float4*>(p);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const float4 x = more ? q[j] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    q[j] = make_float4(x.x + __uint_as_float(o[4 * j]), x.y + __uint_as_float(o[4 * j + 1]),
+                       x.z + __uint_as_float(o[4 * j + 2]), x.w + __uint_as_float(o[4 * j + 3]));
+  }
+}
+
 // A barrier of several warps with a bounded wait: false if it ran out. `phase`
 // counts the warp's passes.
 __device__ __forceinline__ bool meet(uint64_t* bar, unsigned& phase) {
@@ -193,6 +212,12 @@ __device__ __forceinline__ bool meet(uint64_t* bar, unsigned& phase) {
 }
 
 constexpr float kRescale = 8.0f;  // log2 of the weights' bound before the maximum moves
+// The tensor core truncates when it adds to an accumulator: 1 to 2 x 2^-26 of
+// the output is lost with every product, always towards zero (measured on
+// constant and on random values). After kFlush steps a stage adds its
+// accumulator to the segment's record in fp32 and starts a new one, so the loss
+// stays below 5e-6 (1.3e-5 over a segment of 55 steps without).
+constexpr int kFlush = 16;
 
 template <int D>
 __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
@@ -376,7 +401,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
         auto pv = [&](int i) {
           const int st = i & 1, kt = two ? i >> 1 : i;
           const unsigned idx = li0 + 2u * kt + 1u, slot = idx % NST;
-          const bool first = i < 2;  // the stage's first step of the segment
+          const bool first = (i >> 1) % kFlush == 0;  // a new accumulator
           if (!two || st == 0) ok = ok && mbar_wait(&tail.full[slot], (idx / NST) & 1u);
           // the accumulators of the segment before have been read
           if (i == 0 && seg > 0) ok = ok && mbar_wait(&tail.ofree, (seg - 1) & 1);
@@ -436,6 +461,9 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       const int nt = s.t1 - s.t0, steps = two ? nt : (nt + 1 - st) / 2;
       const int valid = two ? s.rows - st * 128 : s.rows;  // query rows of the stage's tile
       const bool idle = quarter * 32 >= valid;             // none in this warp
+      // the stage's record row (with one query tile, stage 1's is scratch behind
+      // it, within the rows that are the CTA's at this point)
+      float* mine = P.W.rec + (s.rec + st * 128 + r) * D;
       float m = -INFINITY, l = 0.0f;
       // Before its first scores can be there, a warp runs a step on whatever its
       // TMEM holds, without storing, waiting or signalling: the instructions are
@@ -495,6 +523,17 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
 #pragma unroll
               for (int j = 0; j < 16; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
               tc_st16(oa + st * 128 + 16 * k, o);
+              if (i > kFlush && r < valid) scale_record(mine + 16 * k, f);
+            }
+          }
+          if (i > 0 && i % kFlush == 0) {
+            tc_wait_st();
+#pragma unroll 1
+            for (int k = 0; k < D / 16; k++) {
+              unsigned o[16];
+              tc_ld16(oa + st * 128 + 16 * k, o);
+              tc_wait_ld();
+              if (r < valid) add_record(mine + 16 * k, o, i > kFlush);
             }
           }
           neg = -m;
@@ -551,6 +590,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       }
       const bool has = two || merge || st == 0;  // columns to write
       const int s0 = two ? st : 0;               // the (first) accumulator
+      const int steps0 = two ? nt : (nt + 1) / 2, steps1 = nt / 2;  // of it, and of the second in a merge
       // (a stage without a step waits too: it would run ahead otherwise, and
       // arrive at `ofree` for segments whose accumulators are still being read)
       ok = __all_sync(0xffffffffu, mbar_wait(&tail.o[s0], no[s0] & 1u));
@@ -568,13 +608,19 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
           tc_ld16(oa + s0 * 128 + k, a);
           if (merge) tc_ld16(oa + 128 + k, b);
           tc_wait_ld();
-          float o[2][8];
-#pragma unroll
-          for (int j = 0; j < 16; j++)
-            o[j / 8][j % 8] = merge ? __uint_as_float(a[j]) * f0 + __uint_as_float(b[j]) * f1 : __uint_as_float(a[j]);
           if (r < valid) {
-            st_global_v8(P.W.rec + row * D + k, o[0]);
-            st_global_v8(P.W.rec + row * D + k + 8, o[1]);
+            float* rec = P.W.rec + row * D + k;
+            float o[2][8];
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+              float x = __uint_as_float(a[j]), y = merge ? __uint_as_float(b[j]) : 0.0f;
+              // (written by this row's thread of either stage, before their merge)
+              if (steps0 > kFlush) x += rec[j];
+              if (merge && steps1 > kFlush) y += rec[128 * D + j];
+              o[j / 8][j % 8] = merge ? x * f0 + y * f1 : x;
+            }
+            st_global_v8(rec, o[0]);
+            st_global_v8(rec + 8, o[1]);
           }
         }
         if (r < valid && (two || st == 0)) P.W.ml[row] = make_float2(m, l);

@@ -64,6 +64,9 @@ __device__ __forceinline__ void group_work(const SharedParams& P, SharedGroup& g
 // of at least kOwnPiece chunks of one (sequence, KV head), about kOwnPieces a
 // warp when there are many.
 constexpr int kOwnPiece = 6, kOwnPieces = 6;
+// Chunks after which a piece's accumulator is added to its fp32 sum: the tensor
+// core truncates with every product added (see kFlush in vattn_prefix_tc.cuh).
+constexpr int kOwnFlush = 32;
 constexpr int kOwnChunk = 16;
 __device__ __forceinline__ int own_chunks(int start, int n) {
   return n > start ? (n - (start & ~15) + kOwnChunk - 1) / kOwnChunk : 0;
@@ -731,11 +734,20 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
             qf[kt][e] = ra < G ? v : 0u;
           }
       }
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[KT][4];
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[KT][4], sum[KT][4];
 #pragma unroll
       for (int mt = 0; mt < KT; mt++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) o[mt][e] = 0.0f;
+        for (int e = 0; e < 4; e++) o[mt][e] = sum[mt][e] = 0.0f;
+      auto flush = [&]() {
+#pragma unroll
+        for (int mt = 0; mt < KT; mt++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            sum[mt][e] += o[mt][e];
+            o[mt][e] = 0.0f;
+          }
+      };
 #pragma unroll 1
       for (int x = 0; x < cu.chunks; x++) {
         issue();  // into the stage that the chunk before left
@@ -794,7 +806,10 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
 #pragma unroll
           for (int mt = 0; mt < KT; mt++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) o[mt][e] *= f[e & 1];
+            for (int e = 0; e < 4; e++) {
+              o[mt][e] *= f[e & 1];
+              sum[mt][e] *= f[e & 1];
+            }
         }
         float pv[4];
 #pragma unroll
@@ -816,9 +831,11 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
           mma_bf16(o[mt], a, ph0, ph1);
           mma_bf16(o[mt], a, pl0, pl1);
         }
+        if ((x + 1) % kOwnFlush == 0) flush();
         __syncwarp();  // the stage is free again
       }
       if (!ok) break;
+      flush();
       // the piece's record: lane holds dims 16 mt + lane / 4 (+ 8)
       // of heads hc, hc + 1
 #pragma unroll
@@ -833,8 +850,8 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
         float* r = P.W.own_rec + (rec + hc + k) * D + ra;
 #pragma unroll
         for (int mt = 0; mt < KT; mt++) {
-          r[16 * mt] = o[mt][k];
-          r[16 * mt + 8] = o[mt][2 + k];
+          r[16 * mt] = sum[mt][k];
+          r[16 * mt + 8] = sum[mt][2 + k];
         }
       }
     }
