@@ -30,7 +30,7 @@ template <typename T, int D, int G>
 SharedKernels kernels_for(bool host_kv) {
   using vattn::kModeSuffix;
   SharedKernels k;
-  k.prefix = vattn::k_shared_prefix<T, D>;
+  k.prefix = host_kv ? vattn::k_shared_prefix<T, D, true> : vattn::k_shared_prefix<T, D, false>;
   k.RB = vattn::PrefixShape<D>::RB;
   k.KT = vattn::PrefixShape<D>::KT;
   k.tc = false;
@@ -191,6 +191,12 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
   P.RB = k.RB;
   P.KT = k.KT;
   P.own_warps = ctx->shared.own_warps;
+  // The tensor-core kernel reads a prefix at the gather's rate, and over the host
+  // link every byte counts: two sequences are enough. The fp32 kernel takes as
+  // long as the gather takes for 4.7, 3.7 and 2.2 sequences with 1, 4 and 8
+  // query heads per KV head (16384 keys x 8 heads, d = 128: 91 to 94 us against
+  // 19.5, 24.5 and 41 us a sequence).
+  P.min_reach = k.tc || P.D.kv_host ? 2 : ctx->G < 4 ? 5 : ctx->G < 8 ? 4 : 3;
   if (!k.own && !P.D.kv_host)
     if (const int rc = vattn::encode_row_maps(c, k_cache, v_cache, num_pages, &P.D)) return ctx->last_status = rc;
   if (k.tc)

@@ -13,8 +13,8 @@
 // and tiles of KT keys on the other. Work is flattened as [group][row block]
 // [KV head][key tile] and cut evenly over a persistent grid; each (CTA, block,
 // head) segment leaves one record (maximum, weight sum, weighted values) per
-// row. Only groups of which two sequences at least reach the end of the prefix
-// are shared: the others, and sequences shorter than their prefix, are left to
+// row. Only groups of which min_reach sequences reach the end of the prefix are
+// shared: the others, and sequences shorter than their prefix, are left to
 // the own part whole, so that no row of a segment is masked and every key of a
 // tile counts for every row.
 #pragma once
@@ -41,6 +41,7 @@ struct SharedParams {
   int RB, KT;  // rows of a block, keys of a tile
   int box;     // rows of a cache box: a power of two that divides the page size, at most KT
   int own_warps;  // k_shared_own's warps; 0: the gather takes the own positions
+  int min_reach;  // sequences that have to reach a prefix's end for it to be shared, at least 2
 };
 
 // ---------------------------------------------------------------- groups
@@ -159,7 +160,7 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
         if (prefix < 0 || prefix > D.max_ctx) {
           n = 0;
         } else if (n >= prefix && prefix > 0) {
-          if (count_reach(P, P.group_start[g], P.group_start[g + 1], prefix) >= 2) start = prefix;
+          if (count_reach(P, P.group_start[g], P.group_start[g + 1], prefix) >= P.min_reach) start = prefix;
         }
       }
       // only the positions behind the prefix are read through this row
@@ -184,7 +185,7 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
         if (lane == 0) atomicOr(D.err, kDevBadGroup);
       } else {
         ok = 1;
-        if (count_reach(P, b0, b1, prefix) >= 2 && bad_pages(P, b0, 0, (prefix + D.ps - 1) / D.ps)) {
+        if (count_reach(P, b0, b1, prefix) >= P.min_reach && bad_pages(P, b0, 0, (prefix + D.ps - 1) / D.ps)) {
           if (lane == 0) atomicOr(D.err, kDevBadPage);
           ok = 0;
         }
@@ -256,7 +257,7 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
         rec.b0 = start_of(g);
         rec.size = start_of(g + 1) - rec.b0;
         rec.prefix = prefix_of(g);
-        if (reach_of(g) >= 2) group_work(P, rec, t, r);
+        if (reach_of(g) >= P.min_reach) group_work(P, rec, t, r);
       }
       const long long it = block_scan_ll(t, s_w), ir = block_scan_ll(r, s_w);
       if (g < P.groups) {
@@ -287,7 +288,7 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
     if (b >= D.batch || bad_bounds) return -1;
     const int g = group_of(b), n = len(b), prefix = prefix_of(g);
     if (n <= 0 || prefix < 0 || prefix > D.max_ctx) return -1;
-    return prefix > 0 && n >= prefix && reach_of(g) >= 2 ? prefix : 0;
+    return prefix > 0 && n >= prefix && reach_of(g) >= P.min_reach ? prefix : 0;
   };
   if (P.own_warps) {
     long long sum = 0;  // chunks of one KV head
@@ -410,27 +411,39 @@ __device__ __forceinline__ int group_at(const SharedParams& P, const SharedGroup
   return 0;
 }
 
+// 16 bytes global -> shared past L1; zeros instead when !in
+__device__ __forceinline__ void cp_async16_or_zero(float* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"(__cvta_generic_to_global(src)), "r"(in ? 16 : 0)
+               : "memory");
+}
+
 // ============================================================ k_shared_prefix
-// fp32 caches, and caches in host memory: fp32 FMAs. Blocks of 64 rows against
-// tiles of 64 keys; 256 threads as 16 x 16, each with 4 x 4 scores and 4 rows
-// of D / 16 outputs, all operands in shared memory as fp32.
+// fp32 caches, and caches in host memory: fp32 FMAs, bound by them from a few
+// sequences on (32 sequences x 4 heads over 16384 keys, d = 128: 8.6 GFLOP in
+// 0.25 ms, 34 TFLOP/s). Blocks of 64 rows against tiles of 64 keys; 256 threads as
+// 16 x 16, each with 4 x 4 scores and 4 rows of D / 16 outputs, all operands in
+// shared memory as fp32.
 template <int D>
 struct PrefixShape {
   static constexpr int RB = 64, KT = 64;
   static constexpr int LD = D + 4;    // row pitch of Q and K: 16-byte rows that start in different banks
   static constexpr int LP = KT + 4;
-  static constexpr size_t SMEM = static_cast<size_t>(RB * LD + KT * LD + KT * D + RB * LP) * 4;
+  static constexpr int TILE = KT * LD + KT * D;  // K and V of a tile
+  static constexpr size_t SMEM = static_cast<size_t>(RB * LD + 2 * TILE + RB * LP) * 4;
+  static_assert(SMEM <= 227 * 1024, "shared memory of the prefix kernel");
 };
 
-template <typename T, int D>
+template <typename T, int D, bool HOST>
 __global__ void __launch_bounds__(256, 1) k_shared_prefix(const __grid_constant__ SharedParams P) {
   using S = PrefixShape<D>;
   constexpr int RB = S::RB, KT = S::KT, LD = S::LD, LP = S::LP, E = Elem<T>::kPer16, VPR = D / E;
   extern __shared__ __align__(16) float sm[];
   float* s_q = sm;
-  float* s_k = s_q + RB * LD;
-  float* s_v = s_k + KT * LD;
-  float* s_p = s_v + KT * D;
+  float* s_kv = s_q + RB * LD;  // two tiles
+  float* s_p = s_kv + 2 * S::TILE;
+  // fp32 rows in device memory are copied asynchronously, a tile ahead
+  constexpr bool kAhead = sizeof(T) == 4 && !HOST;
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   grid_dependency_wait();
   const long long Tt = P.W.group[P.groups].tile0;
@@ -466,27 +479,50 @@ __global__ void __launch_bounds__(256, 1) k_shared_prefix(const __grid_constant_
 #pragma unroll
       for (int j = 0; j < D / 16; j++) o[i][j] = 0.0f;
     }
-    for (int t = s.t0; t < s.t1; t++) {
+    // K and V of tile t into buffer t % 2; rows behind the prefix are zeros
+    auto load = [&](int t) {
       const int k0 = t * KT, nk = min(KT, s.prefix - k0);
-      __syncthreads();
+      float* s_k = s_kv + (t & 1) * S::TILE;
+      float* s_v = s_k + KT * LD;
       for (int i = tid; i < KT * VPR; i += 256) {
         const int r = i / VPR, e = i % VPR * E;
-        uint4 kr = make_uint4(0u, 0u, 0u, 0u), vr = kr;
-        if (r < nk) {
-          const size_t off = row_off(P.D, s.b0, s.h, k0 + r, D) + e;
-          kr = ld_gather(static_cast<const T*>(P.D.k) + off);
-          vr = ld_gather(static_cast<const T*>(P.D.v) + off);
-        }
-        float x[E], y[E];
-        Elem<T>::unpack(kr, x);
-        Elem<T>::unpack(vr, y);
+        const size_t off = r < nk ? row_off(P.D, s.b0, s.h, k0 + r, D) + e : 0;
+        if constexpr (kAhead) {
+          cp_async16_or_zero(s_k + r * LD + e, static_cast<const T*>(P.D.k) + off, r < nk);
+          cp_async16_or_zero(s_v + r * D + e, static_cast<const T*>(P.D.v) + off, r < nk);
+        } else {
+          uint4 kr = make_uint4(0u, 0u, 0u, 0u), vr = kr;
+          if (r < nk) {
+            kr = ld_gather(static_cast<const T*>(P.D.k) + off);
+            vr = ld_gather(static_cast<const T*>(P.D.v) + off);
+          }
+          float x[E], y[E];
+          Elem<T>::unpack(kr, x);
+          Elem<T>::unpack(vr, y);
 #pragma unroll
-        for (int j = 0; j < E; j++) {
-          s_k[r * LD + e + j] = x[j];
-          s_v[r * D + e + j] = y[j];
+          for (int j = 0; j < E; j++) {
+            s_k[r * LD + e + j] = x[j];
+            s_v[r * D + e + j] = y[j];
+          }
         }
       }
-      __syncthreads();
+      if constexpr (kAhead) cp_async_commit();
+    };
+    const bool busy = 4 * (ty & ~1) < s.rows;  // the warp has query rows
+    if constexpr (kAhead) load(s.t0);
+    for (int t = s.t0; t < s.t1; t++) {
+      const int nk = min(KT, s.prefix - t * KT);
+      const float* s_k = s_kv + (t & 1) * S::TILE;
+      const float* s_v = s_k + KT * LD;
+      if constexpr (kAhead) {
+        cp_async_wait<0>();
+        __syncthreads();
+        if (t + 1 < s.t1) load(t + 1);  // into the buffer that the tile before left
+      } else {
+        load(t);
+        __syncthreads();
+      }
+      if (!busy) continue;
       float sc[4][4];
 #pragma unroll
       for (int i = 0; i < 4; i++)
@@ -596,6 +632,9 @@ __global__ void __launch_bounds__(256, 1) k_shared_prefix(const __grid_constant_
 // kernel's last CTAs run (which start after k_shared_prep's end) and waits
 // for them only before it ends, so that its own end means both. What
 // k_shared_prep wrote is therefore read past L1.
+// 256 sequences x 150 positions, 8 heads, d = 128 (165 MB): 30 us, 5.5 TB/s; as
+// slices of k_gather_tc, whose rings drain at every end, 73 us, and with the
+// pieces cut statically 55 us.
 template <int D>
 struct OwnShape {
   static constexpr int H = D / 64, KT = D / 16;
@@ -867,7 +906,8 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
 // WR warps per (sequence, query head): fold the records of the prefix segments
 // and of the own parts, 32 at a time: a lane reads one record's maximum and
 // weight sum, then every lane adds its columns of each record under weights
-// that are all known, so that the loads of several records are in flight.
+// that are all known, so that the loads of several records are in flight. Bound
+// by latency: 6 us behind the last record for 8192 rows of 7 records (30 MB).
 constexpr int kSharedCombWarps = 8;
 
 template <int D, int WR>
