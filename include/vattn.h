@@ -276,9 +276,9 @@ int vattn_rope_init(vattn_rope* rope, const vattn_rope_config* cfg);
    with x's strides; otherwise no element of out may be one of x. tokens = 0
    or heads = 0 does nothing. VATTN_EINVAL for a plan that vattn_rope_init did
    not fill, a null pointer, negative sizes or strides, more than 2^30 tokens or
-   2^16 heads, or a stride of out
-   that would make two heads or tokens overlap (smaller than a head, or than
-   all heads of a token). */
+   2^16 heads, or strides of out that do not keep its rows apart (each at least
+   a head; with several tokens and heads, one of them past the span of the
+   other). */
 int vattn_rotate(const vattn_rope* rope, const void* x, void* out, const int32_t* positions,
                  int tokens, int heads, int dtype, long long x_token_stride,
                  long long x_head_stride, long long out_token_stride, long long out_head_stride,
@@ -383,8 +383,8 @@ size_t vattn_workspace_bytes(const vattn_ctx* ctx);
 int vattn_set_timing(vattn_ctx* ctx, int period);
 int vattn_score_pass_ms(vattn_ctx* ctx, double* total_ms, int* count, int reset);
 
-/* Number of kernel launches the last vattn_decode / vattn_dense_decode call
-   enqueued. */
+/* Number of kernel launches the context's last decode (sparse, dense or
+   shared) or append enqueued. */
 int vattn_last_launch_count(const vattn_ctx* ctx);
 
 /* Text for a return code. */

@@ -61,7 +61,8 @@ def _call(plan, tokens=4, heads=8, dtype=_abi.VATTN_BF16, xs=(1024, 128), os=(10
 def test_rotate_refusals_before_any_launch():
     plan = Rotary(head_dim=128).plan
     bad = [dict(tokens=-1), dict(heads=-1), dict(tokens=(1 << 30) + 1), dict(heads=(1 << 16) + 1), dict(dtype=2),
-           dict(x=0), dict(out=0), dict(pos=0), dict(os=(1024, 127)), dict(os=(1023, 128)), dict(xs=(-1, 128)),
+           dict(x=0), dict(out=0), dict(pos=0), dict(os=(1024, 127)), dict(os=(1023, 128)), dict(os=(127, 4096)),
+           dict(os=(128, 511)), dict(xs=(-1, 128)),
            dict(xs=(1024, -128)), dict(out=1 << 20, xs=(2048, 128)), dict(out=1 << 20, xs=(1024, 256))]
     for kw in bad:
         assert _call(plan, **kw) == _abi.VATTN_EINVAL, kw
@@ -142,6 +143,9 @@ def test_rotate_views_in_place_and_unaligned(dtype):
     assert torch.equal(r.rotate(odd, pos), ref)
     heads_first = keep[:, 3:8].transpose(0, 1).contiguous().transpose(0, 1)
     assert torch.equal(r.rotate(heads_first, pos), ref)
+    out = torch.empty(5, 33, 128, dtype=DT[dtype], device="cuda")
+    assert torch.equal(r.rotate(x.contiguous(), pos, out=out.transpose(0, 1)), r.rotate(x.contiguous(), pos))
+    assert torch.equal(r.rotate(heads_first, pos, out=heads_first), ref)    # in place, heads first
 
 
 @pytest.mark.gpu

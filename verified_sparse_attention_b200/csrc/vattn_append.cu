@@ -709,8 +709,9 @@ int vattn_rotate(const vattn_rope* rope, const void* x, void* out, const int32_t
   if (!x || !out || !positions) return VATTN_EINVAL;
   const int D = rope->head_dim;
   if (xt < 0 || xh < 0 || ot < 0 || oh < 0) return VATTN_EINVAL;
-  if (heads > 1 && oh < D) return VATTN_EINVAL;
-  if (tokens > 1 && ot < (heads - 1) * oh + D) return VATTN_EINVAL;
+  // no two rows of out overlap: heads within a token's span, or tokens within a head's
+  if ((heads > 1 && oh < D) || (tokens > 1 && ot < D)) return VATTN_EINVAL;
+  if (heads > 1 && tokens > 1 && ot < (heads - 1) * oh + D && oh < (tokens - 1) * ot + D) return VATTN_EINVAL;
   if (x == out && ((tokens > 1 && xt != ot) || (heads > 1 && xh != oh))) return VATTN_EINVAL;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
         const Segment s = segment_at(P, group, cur, end, gi);
         gi = s.gi;
         cur = s.next;
-          const bool two = s.rows > 128;
+        const bool two = s.rows > 128;
         const int nt = s.t1 - s.t0, n = two ? 2 * nt : nt;
         auto qk = [&](int i) {
           const int st = i & 1, kt = two ? i >> 1 : i;
