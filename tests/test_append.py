@@ -18,6 +18,7 @@ def _fake(proxy="exact", dtype=torch.bfloat16):
     dec.device, dec._index, dec._cache_index = torch.device("cpu"), -1, -1
     dec.num_q_heads, dec.num_kv_heads, dec.head_dim, dec.page_size = 8, 2, 64, 16
     dec.max_batch, dec.max_ctx, dec.pages_per_seq, dec.proxy, dec.dtype, dec.ctx = 4, 100, 7, proxy, dtype, None
+    dec._cache_shape = (2, 16, 64)
     dec._stream = lambda s: 0
     return dec
 
@@ -369,4 +370,29 @@ def test_append_captured_with_growing_lengths():
     assert dec.last_error() == 0
     assert torch.equal(out, want) and torch.equal(x["k_cache"], ref["k_cache"])
     assert torch.equal(x["v_cache"], ref["v_cache"])
+    dec.close()
+
+
+@pytest.mark.gpu
+def test_append_calls_of_one_context_may_overlap():
+    c, max_ctx = _case(dtype="bf16", d=128, Hq=8, Hkv=2, ps=16, new=[400, 300], before=[3, 60], proxy="loki")
+    dec = _decoder("bf16", 128, 8, 2, 16, 2, max_ctx, "loki")
+    rotary = Rotary(head_dim=128)
+
+    def call(x, stream=None):
+        dec.append(x["k"], x["v"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"], x["num_pages"],
+                   cu_tokens=x["cu_tokens"], rotary=rotary, q=x["q"], q_out=x["q_out"],
+                   k_proj_cache=x["k_proj_cache"], proj_basis=x["proj_basis"], stream=stream)
+
+    xs = [_cuda(c) for _ in range(3)]
+    for x in xs:
+        x["q_out"] = torch.empty_like(x["q"])
+    call(xs[0])
+    torch.cuda.synchronize()
+    for x in xs[1:]:
+        call(x, torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert dec.last_error() == 0
+    for x in xs[1:]:
+        assert all(torch.equal(x[k], xs[0][k]) for k in ("k_cache", "v_cache", "k_proj_cache", "q_out"))
     dec.close()

@@ -281,6 +281,26 @@ def test_shared_equals_dense_and_is_reproducible():
     dec.close()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_two_contexts_on_two_streams(dtype):
+    xs = [shared_batch([9, 6], [700 + 50 * i, 90], [(5 * b + i) % 30 for b in range(15)], Hq=8, Hkv=2, d=64, ps=16,
+                       dtype=DT[dtype], seed=i) for i in range(2)]
+    decs = [_decoder(x, dtype, 16) for x in xs]
+    ys = [_cuda(x) for x in xs]
+    ref = [_call(d, y).clone() for d, y in zip(decs, ys)]
+    outs = [torch.zeros_like(r) for r in ref]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for d, y, o, s in zip(decs, ys, outs, streams):
+            _call(d, y, out=o, stream=s)
+    torch.cuda.synchronize()
+    for d, o, r in zip(decs, outs, ref):
+        assert torch.equal(o, r) and d.last_error() == 0
+        d.close()
+
+
 # ------------------------------------------------------------ as they are used together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

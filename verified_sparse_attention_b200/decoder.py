@@ -26,6 +26,7 @@ class SparseDecoder:
         # the device index of the caches (-1: page-locked host memory) and of everything else
         self._index = torch.cuda.current_device() if self.device.index is None else self.device.index
         self._cache_index = -1 if kv_location == "host" else self._index
+        self._cache_shape = (num_kv_heads, page_size, head_dim)
         self.proxy = proxy
         self.dtype = dtype
         cfg = _abi.vattn_config(num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
@@ -96,7 +97,7 @@ class SparseDecoder:
     def _check_caches(self, k_cache, v_cache, page_table, seq_lens, num_pages):
         """The caches, table and lengths of one call; returns its batch."""
         batch = seq_lens.shape[0]
-        shape = (self.num_kv_heads, self.page_size, self.head_dim)
+        shape = self._cache_shape
         self._check_cache("k_cache", k_cache, num_pages, shape, self._cache_index)
         self._check_cache("v_cache", v_cache, num_pages, shape, self._cache_index)
         if batch > self.max_batch:
