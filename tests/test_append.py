@@ -396,3 +396,25 @@ def test_append_calls_of_one_context_may_overlap():
     for x in xs[1:]:
         assert all(torch.equal(x[k], xs[0][k]) for k in ("k_cache", "v_cache", "k_proj_cache", "q_out"))
     dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_basis_at_any_float(d):
+    c, max_ctx = _case(dtype="bf16", d=d, Hq=4, Hkv=2, ps=16, new=[70, 0, 33], before=[5, 9, 0], proxy="loki")
+    dec = _decoder("bf16", d, 4, 2, 16, 3, max_ctx, "loki")
+    got = []
+    for shift in (0, 1):
+        x = _cuda(c)
+        flat = torch.empty(x["proj_basis"].numel() + 1, device="cuda")
+        basis = flat[shift:shift + x["proj_basis"].numel()].view_as(x["proj_basis"])
+        basis.copy_(x["proj_basis"])
+        assert basis.data_ptr() % 16 == 4 * shift
+        dec.append(x["k"], x["v"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"], x["num_pages"],
+                   cu_tokens=x["cu_tokens"], k_proj_cache=x["k_proj_cache"], proj_basis=basis)
+        torch.cuda.synchronize()
+        got.append(x)
+    # the same products in the same order, whatever the access width
+    for k in ("k_cache", "v_cache", "k_proj_cache"):
+        assert torch.equal(got[0][k], got[1][k])
+    dec.close()

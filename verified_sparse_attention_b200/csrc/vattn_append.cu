@@ -305,11 +305,20 @@ struct KeyTile {
   // row pitch: odd in words for the transposed copy's column reads, 16-byte
   // rows for the projection's fragment loads
   static constexpr int LD = PROXY == VATTN_SPARQ ? D + 4 / sizeof(T) : D + 16 / sizeof(T);
+  // shared memory: a head's split basis (bf16 projections), two tiles of keys
+  static constexpr bool SPLIT = PROXY == VATTN_LOKI && sizeof(T) == 2;
+  static constexpr size_t BASIS = SPLIT ? 4 * D * kRank : 0, BYTES = BASIS + 2 * TT * LD * sizeof(T);
 };
 
 __device__ __forceinline__ unsigned smem_addr(const void* p) { return static_cast<unsigned>(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ void ldsm4(unsigned addr, unsigned (&a)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(unsigned addr, unsigned (&a)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
                : "r"(addr)
                : "memory");
@@ -328,13 +337,46 @@ __device__ __forceinline__ unsigned pack2(float lo, float hi) {
 
 // Projected keys of a tile of bf16 keys: [TT tokens x D] . [D x 32] on the
 // tensor cores, the fp32 basis as two bf16 terms: 2^-18 of the summed magnitudes
-// is lost, against the 2^-9 of the bf16 result's own rounding. Every warp has 16
-// tokens and 4 TT / 16 components; the basis comes straight from L2 in operand
-// order. 8190 tokens of 8 heads (71 MB): 27 us, bound by the instructions of the
-// rotation and of splitting the basis; as fp32 FMAs from shared memory 73 us.
+// is lost, against the 2^-9 of the bf16 result's own rounding. The block splits
+// a head's basis once per job into shared memory; every warp has 16 tokens and
+// 4 TT / 16 components. 8190 tokens of 8 heads (71 MB): 25.2 us, of which 5 us
+// go without the projection and 3 without the cosines (each warp splitting its
+// own operands: 27; fp32 FMAs from shared memory: 73). Loaded after the stores,
+// where no other row is held, the basis costs no spill (before them: 27.6);
+// copied a job ahead with cp.async it gains 0.5 us for 16 KB more.
+template <int D, bool VEC>
+struct Basis {
+  static constexpr int N = D * kRank / 4 / kThreads;  // quads of components per thread
+  float4 x[N];
+  __device__ __forceinline__ void load(const float* basis) {
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const float* p = basis + 4 * (i * kThreads + threadIdx.x);
+      if constexpr (VEC)
+        x[i] = __ldg(reinterpret_cast<const float4*>(p));
+      else
+        x[i] = make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+    }
+  }
+  // Rows of 128 bytes, one per key dimension: 16-byte chunk 2 c + term holds
+  // components 8 c to 8 c + 7, at place (2 c + term) ^ (row % 8).
+  __device__ __forceinline__ void split(unsigned char* s) const {
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int at = i * kThreads + threadIdx.x, row = at / (kRank / 4), quad = at % (kRank / 4);
+      const float4 v = x[i];
+      const unsigned h0 = pack2(v.x, v.y), h1 = pack2(v.z, v.w);
+      const unsigned l0 = pack2(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xFFFF0000u));
+      const unsigned l1 = pack2(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xFFFF0000u));
+      unsigned char* o = s + row * 128 + 8 * (quad & 1);
+      *reinterpret_cast<uint2*>(o + (((quad & ~1) ^ (row & 7)) << 4)) = make_uint2(h0, h1);
+      *reinterpret_cast<uint2*>(o + (((quad | 1) ^ (row & 7)) << 4)) = make_uint2(l0, l1);
+    }
+  }
+};
 template <int D, int LD, int TT>
-__device__ __forceinline__ void project_tile(const __nv_bfloat16* s_key, const float* basis, const int* s_row, int n,
-                                             int h, const AppendArgs& A) {
+__device__ __forceinline__ void project_tile(const __nv_bfloat16* s_key, const unsigned char* s_basis,
+                                             const int* s_row, int n, int h, const AppendArgs& A) {
   constexpr int MT = TT / 16, NX = 4 * MT / 8;  // token tiles; 8-component tiles of a warp
   static_assert(kThreads / 32 * NX == 4 * MT && NX >= 1, "warps cover the tile");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -346,21 +388,18 @@ __device__ __forceinline__ void project_tile(const __nv_bfloat16* s_key, const f
 #pragma unroll
     for (int i = 0; i < 4; i++) acc[x][i] = 0.0f;
   const unsigned rows = smem_addr(s_key + (m0 + (lane & 15)) * LD + (lane >> 4) * 8);
-  const float* bp = basis + (2 * (lane & 3)) * kRank + n0 + (lane >> 2);
+  // lanes 0-15 address the first term of 16 rows, lanes 16-31 the second
+  const unsigned brow = smem_addr(s_basis + (lane & 15) * 128);
 #pragma unroll
   for (int k = 0; k < D; k += 16) {
     unsigned a[4];
     ldsm4(rows + k * 2, a);
 #pragma unroll
     for (int x = 0; x < NX; x++) {
-      float b[4];
-#pragma unroll
-      for (int i = 0; i < 4; i++) b[i] = __ldg(bp + (k + (i & 1) + 8 * (i >> 1)) * kRank + 8 * x);
-      const unsigned b0 = pack2(b[0], b[1]), b1 = pack2(b[2], b[3]);
-      mma16816(acc[x], a, b0, b1);
-      mma16816(acc[x], a,
-               pack2(b[0] - __uint_as_float(b0 << 16), b[1] - __uint_as_float(b0 & 0xFFFF0000u)),
-               pack2(b[2] - __uint_as_float(b1 << 16), b[3] - __uint_as_float(b1 & 0xFFFF0000u)));
+      unsigned b[4];
+      ldsm4_t(brow + k * 128 + (((2 * (n0 / 8 + x) + (lane >> 4)) ^ (lane & 7)) << 4), b);
+      mma16816(acc[x], a, b[0], b[1]);
+      mma16816(acc[x], a, b[2], b[3]);
     }
   }
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.k_proj);
@@ -408,14 +447,20 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
   constexpr int NP = D / (2 * E);
   __shared__ int s_seq[kMaxTok], s_pos[kMaxTok];
   __shared__ int s_row[kMaxTok];
+  using Tile = KeyTile<T, D, E, PROXY>;
+  using Table = TurnTable<T, D, E>;
+  // a block is one or the other: the table of cosines, or a tile's keys and the
+  // split basis behind them
+  constexpr size_t kTileBytes = PROXY == VATTN_EXACT ? 0 : Tile::BYTES;
+  __shared__ __align__(128) unsigned char s_raw[kTileBytes > sizeof(Table) ? kTileBytes : sizeof(Table)];
   dependency_wait();
   int blk = blockIdx.x;
   if constexpr (PROXY != VATTN_EXACT) {
     if (blk < A.key_blocks) {
-      using S = KeyTile<T, D, E, PROXY>;
-      constexpr int TT = S::TT, LD = S::LD, LANES = kThreads / NP;  // LANES: tokens at once
+      constexpr int TT = Tile::TT, LD = Tile::LD, LANES = kThreads / NP;  // LANES: tokens at once
       constexpr bool kOnce = TT <= LANES;                           // every thread has one token
-      __shared__ __align__(16) T s_key[2][TT * LD];
+      constexpr bool kSplit = Tile::SPLIT;
+      T* s_key = reinterpret_cast<T*>(s_raw + Tile::BASIS);
       const int jobs = (A.tokens + TT - 1) / TT * A.Hkv;
       const int j0 = static_cast<int>(static_cast<long long>(jobs) * blk / A.key_blocks);
       const int j1 = static_cast<int>(static_cast<long long>(jobs) * (blk + 1) / A.key_blocks);
@@ -448,7 +493,9 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
           mine = lane0 < n && s_row[lane0] >= 0;
           if (kOnce && mine) P.turn(A.rope, p, s_pos[lane0], false);
         }
-        T* key = s_key[(j - j0) & 1];
+        T* key = s_key + ((j - j0) & 1) * (TT * LD);
+        const float* basis = A.basis + static_cast<size_t>(h) * D * kRank;
+        Basis<D, (E > 1)> split;
         auto put = [&](int i, Chunk<T, E> (&c)[4]) {
           if (P.turned) P.apply(c[0], c[1]);
           const size_t at = static_cast<size_t>(s_row[i] + h * A.ps) * D;
@@ -474,6 +521,11 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
             put(i, c);
           }
         }
+        if constexpr (kSplit) {
+          split.load(basis);
+          __syncthreads();  // the job before is done with its basis
+          split.split(s_raw);
+        }
         __syncthreads();  // (the other buffer's readers have passed the sync before)
         if constexpr (PROXY == VATTN_SPARQ) {
           // neighbouring lanes hold neighbouring tokens, whose slots are neighbours too
@@ -485,8 +537,10 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
 #pragma unroll 8
             for (int j = threadIdx.x / TT; j < D; j += kThreads / TT) o[static_cast<size_t>(j) * A.ps] = key[i * LD + j];
           }
+        } else if constexpr (kSplit) {
+          project_tile<D, LD, TT>(key, s_raw, s_row, n, h, A);
         } else {
-          project_tile<D, LD, TT>(key, A.basis + static_cast<size_t>(h) * D * kRank, s_row, n, h, A);
+          project_tile<D, LD, TT>(key, basis, s_row, n, h, A);
         }
       }
       return;
@@ -494,7 +548,7 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
     blk -= A.key_blocks;
   }
   // rows of tok_block tokens: keys, queries and values, or the queries alone
-  __shared__ TurnTable<T, D, E> table;
+  Table& table = *reinterpret_cast<Table*>(s_raw);
   const int hl = kThreads / NP / A.tok_block;
   const int t0 = blk / A.row_y * A.tok_block;
   const int n = min(A.tok_block, A.tokens - t0);
@@ -795,6 +849,7 @@ int vattn_append(vattn_ctx* ctx, const vattn_append_params* prm, const int32_t* 
   a.num_pages = prm->num_pages;
   const int E = c.dtype == VATTN_BF16 ? 8 : 4;
   const bool vec = a.rope.rot_dim / 2 % E == 0 && aligned16(a.k) && aligned16(a.v) && (a.ks | a.vs) % E == 0 &&
+                   (c.proxy != VATTN_LOKI || aligned16(a.basis)) &&
                    (!a.q || (aligned16(a.q) && aligned16(a.q_out) && a.qs % E == 0));
   vattn::DeviceScope scope(ctx->device);
   if (!scope.ok) return ctx->last_status = VATTN_ECUDA;
