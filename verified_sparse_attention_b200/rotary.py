@@ -41,7 +41,8 @@ class Rotary:
 
         x may be strided over tokens and heads. out: a tensor like x (x itself to
         rotate in place); new and contiguous by default. transpose: the transposed
-        rotation, which turns the gradient of the result into that of x.
+        rotation, which turns the gradient of the result into that of x; autograd
+        does not record the call.
         """
         shape, strides, index = x.shape, x.stride(), x.get_device()
         dtype = _DTYPES.get(x.dtype)
