@@ -418,3 +418,28 @@ def test_append_basis_at_any_float(d):
     for k in ("k_cache", "v_cache", "k_proj_cache"):
         assert torch.equal(got[0][k], got[1][k])
     dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_projects_with_the_whole_fp32_basis(d):
+    # keys of one +1 and one -1: the projected key is the difference of two basis entries, which agree but for
+    # their last 12 bits. At most six products (three bf16 terms of each entry, below 2) are not zero, and an
+    # fp32 accumulator loses up to 2^-23 of its magnitude with each; then the result is rounded to bf16. The
+    # stored rotated key is the key itself (no rotation).
+    c, max_ctx = _case(dtype="bf16", d=d, Hq=4, Hkv=2, ps=16, new=[70, 0, 33], before=[5, 9, 0], proxy="loki")
+    g = torch.Generator().manual_seed(3)
+    T = len(c["k"])
+    at = torch.stack([torch.randperm(d, generator=g)[:2] for _ in range(2 * T)]).view(T, 2, 2)
+    c["k"] = torch.zeros(T, 2, d).scatter_(2, at, torch.tensor([1.0, -1.0]).expand(T, 2, 2)).bfloat16()
+    c["proj_basis"] = 1 + torch.rand(2, 1, RANK, generator=g) / 2 + 2**-12 * torch.rand(2, d, RANK, generator=g)
+    dec = _decoder("bf16", d, 4, 2, 16, 3, max_ctx, "loki")
+    x = _cuda(c)
+    dec.append(x["k"], x["v"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"], x["num_pages"],
+               cu_tokens=x["cu_tokens"], k_proj_cache=x["k_proj_cache"], proj_basis=x["proj_basis"])
+    assert dec.last_error() == 0
+    t, _, _, page, slot = (torch.tensor(v, dtype=torch.int64) for v in zip(*_slots(c, [70, 0, 33], 16)))
+    ref = torch.einsum("thd,hdr->thr", c["k"][t].double(), c["proj_basis"].double())
+    err = (x["k_proj_cache"].cpu()[page, :, slot].double() - ref).abs() - 2**-8 * ref.abs()
+    assert float(err.max()) <= 6 * 2**-23 * 2, float(err.max())
+    dec.close()

@@ -307,7 +307,7 @@ struct KeyTile {
   static constexpr int LD = PROXY == VATTN_SPARQ ? D + 4 / sizeof(T) : D + 16 / sizeof(T);
   // shared memory: a head's split basis (bf16 projections), two tiles of keys
   static constexpr bool SPLIT = PROXY == VATTN_LOKI && sizeof(T) == 2;
-  static constexpr size_t BASIS = SPLIT ? 4 * D * kRank : 0, BYTES = BASIS + 2 * TT * LD * sizeof(T);
+  static constexpr size_t BASIS = SPLIT ? 6 * D * kRank : 0, BYTES = BASIS + 2 * TT * LD * sizeof(T);
 };
 
 __device__ __forceinline__ unsigned smem_addr(const void* p) { return static_cast<unsigned>(__cvta_generic_to_shared(p)); }
@@ -336,10 +336,11 @@ __device__ __forceinline__ unsigned pack2(float lo, float hi) {
 }
 
 // Projected keys of a tile of bf16 keys: [TT tokens x D] . [D x 32] on the
-// tensor cores, the fp32 basis as two bf16 terms: 2^-18 of the summed magnitudes
-// is lost, against the 2^-9 of the bf16 result's own rounding. The block splits
+// tensor cores, the fp32 basis as three bf16 terms, which hold its 24 bits whole:
+// the products are exact and summed in fp32. (Two terms lose 2^-17 of a basis
+// entry; that moved one bf16 result in 400 to its neighbour.) The block splits
 // a head's basis once per job into shared memory; every warp has 16 tokens and
-// 4 TT / 16 components. 8190 tokens of 8 heads (71 MB): 25.2 us, of which 5 us
+// 4 TT / 16 components. 8190 tokens of 8 heads (71 MB): 26.2 us (two terms: 25.2), of which 6 us
 // go without the projection and 3 without the cosines (each warp splitting its
 // own operands: 27; fp32 FMAs from shared memory: 73). Loaded after the stores,
 // where no other row is held, the basis costs no spill (before them: 27.6);
@@ -358,21 +359,27 @@ struct Basis {
         x[i] = make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
     }
   }
-  // Rows of 128 bytes, one per key dimension: 16-byte chunk 2 c + term holds
-  // components 8 c to 8 c + 7, at place (2 c + term) ^ (row % 8).
+  // The first two terms: rows of 128 bytes, one per key dimension, whose 16-byte
+  // chunk 2 c + term holds components 8 c to 8 c + 7, at place
+  // (2 c + term) ^ (row % 8). The third behind them: rows of 64 bytes, chunk c at
+  // place c ^ (row / 2 % 4). Eight rows of one chunk lie in different banks.
   __device__ __forceinline__ void split(unsigned char* s) const {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int at = i * kThreads + threadIdx.x, row = at / (kRank / 4), quad = at % (kRank / 4);
       const float4 v = x[i];
       const unsigned h0 = pack2(v.x, v.y), h1 = pack2(v.z, v.w);
-      const unsigned l0 = pack2(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xFFFF0000u));
-      const unsigned l1 = pack2(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xFFFF0000u));
+      const float4 r = make_float4(v.x - low(h0), v.y - high(h0), v.z - low(h1), v.w - high(h1));
+      const unsigned l0 = pack2(r.x, r.y), l1 = pack2(r.z, r.w);
       unsigned char* o = s + row * 128 + 8 * (quad & 1);
       *reinterpret_cast<uint2*>(o + (((quad & ~1) ^ (row & 7)) << 4)) = make_uint2(h0, h1);
       *reinterpret_cast<uint2*>(o + (((quad | 1) ^ (row & 7)) << 4)) = make_uint2(l0, l1);
+      *reinterpret_cast<uint2*>(s + D * 128 + row * 64 + (((quad >> 1) ^ (row >> 1 & 3)) << 4) + 8 * (quad & 1)) =
+          make_uint2(pack2(r.x - low(l0), r.y - high(l0)), pack2(r.z - low(l1), r.w - high(l1)));
     }
   }
+  __device__ static __forceinline__ float low(unsigned h) { return __uint_as_float(h << 16); }
+  __device__ static __forceinline__ float high(unsigned h) { return __uint_as_float(h & 0xFFFF0000u); }
 };
 template <int D, int LD, int TT>
 __device__ __forceinline__ void project_tile(const __nv_bfloat16* s_key, const unsigned char* s_basis,
@@ -390,16 +397,25 @@ __device__ __forceinline__ void project_tile(const __nv_bfloat16* s_key, const u
   const unsigned rows = smem_addr(s_key + (m0 + (lane & 15)) * LD + (lane >> 4) * 8);
   // lanes 0-15 address the first term of 16 rows, lanes 16-31 the second
   const unsigned brow = smem_addr(s_basis + (lane & 15) * 128);
+  // the third term of 32 rows, a row per lane
+  const unsigned crow = smem_addr(s_basis + D * 128 + lane * 64);
 #pragma unroll
-  for (int k = 0; k < D; k += 16) {
-    unsigned a[4];
-    ldsm4(rows + k * 2, a);
+  for (int k = 0; k < D; k += 32) {
+    unsigned a[2][4];
+    ldsm4(rows + k * 2, a[0]);
+    ldsm4(rows + k * 2 + 32, a[1]);
 #pragma unroll
     for (int x = 0; x < NX; x++) {
-      unsigned b[4];
-      ldsm4_t(brow + k * 128 + (((2 * (n0 / 8 + x) + (lane >> 4)) ^ (lane & 7)) << 4), b);
-      mma16816(acc[x], a, b[0], b[1]);
-      mma16816(acc[x], a, b[2], b[3]);
+      unsigned c[4];
+      ldsm4_t(crow + k * 64 + (((n0 / 8 + x) ^ (lane >> 1 & 3)) << 4), c);
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        unsigned b[4];
+        ldsm4_t(brow + (k + 16 * i) * 128 + (((2 * (n0 / 8 + x) + (lane >> 4)) ^ (lane & 7)) << 4), b);
+        mma16816(acc[x], a[i], b[0], b[1]);
+        mma16816(acc[x], a[i], b[2], b[3]);
+        mma16816(acc[x], a[i], c[2 * i], c[2 * i + 1]);
+      }
     }
   }
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.k_proj);
