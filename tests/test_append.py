@@ -443,3 +443,25 @@ def test_append_projects_with_the_whole_fp32_basis(d):
     err = (x["k_proj_cache"].cpu()[page, :, slot].double() - ref).abs() - 2**-8 * ref.abs()
     assert float(err.max()) <= 6 * 2**-23 * 2, float(err.max())
     dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("length", [-2**31, -2**31 + 1, -2**31 + 3, 2**31 - 1])
+def test_append_skips_and_reports_lengths_at_the_ends_of_int32(length):
+    c, max_ctx = _case(dtype="bf16", d=64, Hq=8, Hkv=2, ps=16, new=[20, 3, 4, 2], before=[0, 10, 0, 5], proxy="exact")
+    dec = _decoder("bf16", 64, 8, 2, 16, 4, max_ctx, "exact")
+    lens = c["seq_lens"].clone()
+    lens[1] = length
+    for rows, cu in ((slice(None), c["cu_tokens"].cuda()), (slice(4), None)):   # ragged, and one token each
+        got = []
+        for seq_lens in (c["seq_lens"], lens):
+            x = _cuda(dict(c, seq_lens=seq_lens))
+            dec.append(x["k"][rows], x["v"][rows], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"],
+                       x["num_pages"], cu_tokens=cu)
+            assert dec.last_error() == (0 if seq_lens is c["seq_lens"] else _abi.VATTN_DEV_BAD_SEQLEN)
+            got.append([x["k_cache"].cpu(), x["v_cache"].cpu()])
+        page = int(c["page_table"][1, 0])
+        for name, good, bad in zip(("k_cache", "v_cache"), *got):
+            good[page] = c[name][page]
+            assert torch.equal(bad, good)
+    dec.close()

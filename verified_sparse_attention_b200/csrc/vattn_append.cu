@@ -253,14 +253,14 @@ __device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_p
       }
       const int e = min(hi, t0 + n);
       if (e <= max(lo, t0)) continue;
-      const int len = A.seq_lens[b], before = len - (hi - lo);
-      if (before < 0 || len > A.max_ctx) {
+      const int len = A.seq_lens[b];  // any int: compared before anything is subtracted from it
+      if (len < hi - lo || len > A.max_ctx) {
         atomicOr(A.err, kDevBadSeqlen);
         continue;
       }
       for (int t = max(lo, t0); t < e; t++) {
         s_seq[t - t0] = b;
-        s_pos[t - t0] = before + (t - lo);
+        s_pos[t - t0] = len - (hi - lo) + (t - lo);
       }
     }
     __syncthreads();
@@ -273,11 +273,12 @@ __device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_p
       pos = b < 0 ? -1 : s_pos[i];
     } else {
       b = t0 + i;
-      pos = A.seq_lens[b] - 1;
-      if (pos < -1 || pos >= A.max_ctx) {
+      int len = A.seq_lens[b];
+      if (len < 0 || len > A.max_ctx) {
         atomicOr(A.err, kDevBadSeqlen);
-        pos = -1;
+        len = 0;
       }
+      pos = len - 1;
       s_pos[i] = pos;
     }
     if (pos >= 0) {
