@@ -302,7 +302,8 @@ int vattn_rotate(const vattn_rope* rope, const void* x, void* out, const int32_t
  * Slots must differ: two tokens with one slot (a page listed twice) race.
  * Device-side violations never trap: a sequence with n_b < 0, rows outside
  * [0, tokens), seq_lens[b] < n_b or seq_lens[b] > max_ctx sets
- * VATTN_DEV_BAD_SEQLEN and is skipped; a token whose page id is out of range sets
+ * VATTN_DEV_BAD_SEQLEN and is skipped (rows that descending bounds give to several
+ * sequences go to the first that is not); a token whose page id is out of range sets
  * VATTN_DEV_BAD_PAGE and is skipped (its q_out row too). */
 typedef struct {
   const vattn_rope* rope;   /* host; NULL: k and q are taken as they are          */

@@ -465,3 +465,30 @@ def test_append_skips_and_reports_lengths_at_the_ends_of_int32(length):
             good[page] = c[name][page]
             assert torch.equal(bad, good)
     dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("proxy", ["exact", "sparq"])
+def test_append_bounds_that_descend(proxy):
+    # sequence 1's bounds descend: it is skipped, and the rows that sequences 0 and 2 both claim are sequence 0's
+    new = [30, 5, 20, 7]
+    c, max_ctx = _case(dtype="bf16", d=64, Hq=8, Hkv=2, ps=16, new=new, before=[3, 10, 30, 0], proxy=proxy, pad=5)
+    dec = _decoder("bf16", 64, 8, 2, 16, 4, max_ctx, proxy)
+    cu = torch.tensor([0, 30, 22, 42, 49], dtype=torch.int32)
+    want = {k: c[k].clone() for k in ("k_cache", "v_cache")}
+    q_want = torch.full_like(c["q"], 7.0)
+    for b, rows in ((0, range(30)), (2, range(30, 42)), (3, range(42, 49))):
+        for t in rows:
+            p = int(c["seq_lens"][b]) - int(cu[b + 1]) + t
+            page, slot = int(c["page_table"][b, p // 16]), p % 16
+            want["k_cache"][page, :, slot], want["v_cache"][page, :, slot] = c["k"][t], c["v"][t]
+            q_want[t] = c["q"][t]
+    for _ in range(5):
+        x = _cuda(c)
+        out = torch.full_like(x["q"], 7.0)
+        dec.append(x["k"], x["v"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"], x["num_pages"],
+                   cu_tokens=cu.cuda(), q=x["q"], q_out=out, k_t_cache=x["k_t_cache"])
+        assert dec.last_error() == _abi.VATTN_DEV_BAD_SEQLEN
+        assert torch.equal(x["k_cache"].cpu(), want["k_cache"]) and torch.equal(x["v_cache"].cpu(), want["v_cache"])
+        assert torch.equal(out.cpu(), q_want)
+    dec.close()

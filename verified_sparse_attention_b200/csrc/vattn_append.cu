@@ -240,37 +240,61 @@ struct AppendArgs {
 
 // Position and cache row (page * Hkv * ps + slot; -1: nothing to write) of
 // tokens [t0, t0 + n) into shared memory, by the whole block. Every sequence
-// marks its own tokens of the range, in one round of loads.
+// marks its own tokens of the range, in one round of loads. Only bounds that
+// descend can give a token to several: then the first of these has it, found in
+// a second round.
 __device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_pos, int* s_row) {
+  constexpr int kNone = 0x7FFFFFFF;
   if (A.cu != nullptr) {
-    for (int i = threadIdx.x; i < n; i += blockDim.x) s_seq[i] = -1;
+    // calls take(b, first, last, position of token 0) for every sequence with tokens of the range
+    auto sequences = [&](bool report, auto take) -> bool {
+      bool bad = false;
+      for (int b = threadIdx.x; b < A.batch; b += blockDim.x) {
+        const int lo = A.cu[b], hi = A.cu[b + 1];
+        if (lo < 0 || hi < lo || hi > A.tokens) {
+          if (report && t0 == 0) atomicOr(A.err, kDevBadSeqlen);
+          bad = true;
+          continue;
+        }
+        const int e = min(hi, t0 + n);
+        if (e <= max(lo, t0)) continue;
+        const int len = A.seq_lens[b];  // any int: compared before anything is subtracted from it
+        if (len < hi - lo || len > A.max_ctx) {
+          if (report) atomicOr(A.err, kDevBadSeqlen);
+          continue;
+        }
+        take(b, max(lo, t0), e, len - hi);
+      }
+      return bad;
+    };
+    for (int i = threadIdx.x; i < n; i += blockDim.x) s_seq[i] = kNone;
     __syncthreads();
-    for (int b = threadIdx.x; b < A.batch; b += blockDim.x) {
-      const int lo = A.cu[b], hi = A.cu[b + 1];
-      if (lo < 0 || hi < lo || hi > A.tokens) {
-        if (t0 == 0) atomicOr(A.err, kDevBadSeqlen);
-        continue;
-      }
-      const int e = min(hi, t0 + n);
-      if (e <= max(lo, t0)) continue;
-      const int len = A.seq_lens[b];  // any int: compared before anything is subtracted from it
-      if (len < hi - lo || len > A.max_ctx) {
-        atomicOr(A.err, kDevBadSeqlen);
-        continue;
-      }
-      for (int t = max(lo, t0); t < e; t++) {
+    const bool bad = sequences(true, [&](int b, int t, int e, int base) {
+      for (; t < e; t++) {
         s_seq[t - t0] = b;
-        s_pos[t - t0] = len - (hi - lo) + (t - lo);
+        s_pos[t - t0] = base + t;
       }
+    });
+    if (__syncthreads_or(bad)) {
+      for (int i = threadIdx.x; i < n; i += blockDim.x) s_seq[i] = kNone;
+      __syncthreads();
+      sequences(false, [&](int b, int t, int e, int) {
+        for (; t < e; t++) atomicMin(&s_seq[t - t0], b);
+      });
+      __syncthreads();
+      sequences(false, [&](int b, int t, int e, int base) {
+        for (; t < e; t++)
+          if (s_seq[t - t0] == b) s_pos[t - t0] = base + t;
+      });
+      __syncthreads();
     }
-    __syncthreads();
   }
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     int row = -1;  // below 2^31, as the host checked
     int b, pos;
     if (A.cu != nullptr) {
       b = s_seq[i];
-      pos = b < 0 ? -1 : s_pos[i];
+      pos = b == kNone ? -1 : s_pos[i];
     } else {
       b = t0 + i;
       int len = A.seq_lens[b];
