@@ -492,3 +492,21 @@ def test_append_bounds_that_descend(proxy):
         assert torch.equal(x["k_cache"].cpu(), want["k_cache"]) and torch.equal(x["v_cache"].cpu(), want["v_cache"])
         assert torch.equal(out.cpu(), q_want)
     dec.close()
+
+
+@pytest.mark.gpu
+def test_append_reports_bad_lengths_of_sequences_without_new_tokens():
+    c, max_ctx = _case(dtype="bf16", d=64, Hq=8, Hkv=2, ps=16, new=[70, 0, 5], before=[0, 10, 3], proxy="exact")
+    dec = _decoder("bf16", 64, 8, 2, 16, 3, max_ctx, "exact")
+    got = []
+    for length in (10, 0, -1, max_ctx + 1):
+        lens = c["seq_lens"].clone()
+        lens[1] = length
+        x = _cuda(dict(c, seq_lens=lens))
+        dec.append(x["k"], x["v"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"], x["num_pages"],
+                   cu_tokens=x["cu_tokens"])
+        assert dec.last_error() == (0 if 0 <= length <= max_ctx else _abi.VATTN_DEV_BAD_SEQLEN), length
+        got.append(x)
+    for x in got[1:]:
+        assert torch.equal(x["k_cache"], got[0]["k_cache"]) and torch.equal(x["v_cache"], got[0]["v_cache"])
+    dec.close()

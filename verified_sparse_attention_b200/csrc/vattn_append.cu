@@ -257,13 +257,15 @@ __device__ void resolve(const AppendArgs& A, int t0, int n, int* s_seq, int* s_p
           continue;
         }
         const int e = min(hi, t0 + n);
-        if (e <= max(lo, t0)) continue;
+        // (the first tokens' block checks the lengths of sequences without new tokens too)
+        const bool any = e > max(lo, t0);
+        if (!any && t0 > 0) continue;
         const int len = A.seq_lens[b];  // any int: compared before anything is subtracted from it
         if (len < hi - lo || len > A.max_ctx) {
           if (report) atomicOr(A.err, kDevBadSeqlen);
           continue;
         }
-        take(b, max(lo, t0), e, len - hi);
+        if (any) take(b, max(lo, t0), e, len - hi);
       }
       return bad;
     };
