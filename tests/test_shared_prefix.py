@@ -301,6 +301,25 @@ def test_shared_two_contexts_on_two_streams(dtype):
         d.close()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv_location", [("bf16", "device"), ("f32", "device"), ("f32", "host")])
+def test_shared_output_at_any_float(dtype, kv_location):
+    x = shared_batch([3, 2], [200, 77], [1, 20, 0, 5, 40], Hq=8, Hkv=2, d=64, ps=16, dtype=DT[dtype])
+    dec = _decoder(x, dtype, 16, kv_location=kv_location)
+    y = _cuda(x)
+    if kv_location == "host":
+        y["k_cache"], y["v_cache"] = x["k_cache"].pin_memory(), x["v_cache"].pin_memory()
+    ref = _call(dec, y)
+    flat = torch.full((ref.numel() + 4,), 3.0, device="cuda")
+    for shift in range(4):
+        flat.fill_(3.0)
+        _call(dec, y, out=flat[shift:shift + ref.numel()].view_as(ref))
+        assert torch.equal(flat[shift:shift + ref.numel()].view_as(ref), ref)
+        assert (flat[:shift] == 3).all() and (flat[shift + ref.numel():] == 3).all()
+    assert dec.last_error() == 0
+    dec.close()
+
+
 # ------------------------------------------------------------ as they are used together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

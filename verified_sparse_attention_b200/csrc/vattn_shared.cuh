@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
   const int b = real ? row_out / Q.Hq : 0, hq = row_out % Q.Hq, h = hq / Q.G, gh = hq % Q.G, u = b * Q.Hkv + h;
   const int4 i0 = __ldcg(reinterpret_cast<const int4*>(Q.info + u));  // n, s1, wst, k
   const int n_pos = i0.x, start = i0.y, gi = i0.w;
-  float2* out = reinterpret_cast<float2*>(Q.out + static_cast<size_t>(row_out) * D);
+  float* out = Q.out + static_cast<size_t>(row_out) * D;
   const bool shared = start > 0;
   const bool none = n_pos <= 0 || (shared && !__ldcg(P.W.pages_ok + gi));
   // records of the own part
@@ -1056,8 +1056,16 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
   }
   if (!real) return;
 #pragma unroll
-  for (int i = 0; i < PL; i++)
-    out[lane + 32 * i] = none ? make_float2(0.0f, 0.0f) : make_float2(a[i].x / l, a[i].y / l);
+  for (int i = 0; i < PL; i++) {
+    const float2 v = none ? make_float2(0.0f, 0.0f) : make_float2(a[i].x / l, a[i].y / l);
+    float* p = out + 2 * (lane + 32 * i);
+    if ((reinterpret_cast<uintptr_t>(Q.out) & 7u) == 0) {
+      *reinterpret_cast<float2*>(p) = v;
+    } else {  // the caller's array may start at any float
+      p[0] = v.x;
+      p[1] = v.y;
+    }
+  }
 }
 
 }  // namespace vattn
