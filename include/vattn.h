@@ -275,7 +275,8 @@ int vattn_rope_init(vattn_rope* rope, const vattn_rope_config* cfg);
    amplitude): the gradient of x from the gradient of out. out may be x itself
    with x's strides; otherwise no element of out may be one of x. tokens = 0
    or heads = 0 does nothing. VATTN_EINVAL for a plan that vattn_rope_init did
-   not fill, a null pointer, negative sizes or strides, more than 2^30 tokens or
+   not fill, a pointer that is null or not at a multiple of its element's size,
+   negative sizes or strides, more than 2^30 tokens or
    2^16 heads, or strides of out that do not keep its rows apart (each at least
    a head; with several tokens and heads, one of them past the span of the
    other). */
@@ -326,7 +327,9 @@ typedef struct {
 
 /* Enqueued on `stream` of the context's device (whichever device is current),
    one launch, no workspace, so calls on one context may overlap. Host-resident
-   caches (VATTN_KV_HOST) are written over the host link. */
+   caches (VATTN_KV_HOST) are written over the host link. The caches start at
+   multiples of 16 bytes, the other arrays at multiples of their element's size
+   (else VATTN_EINVAL); rows at multiples of 16 bytes move in wider pieces. */
 int vattn_append(vattn_ctx* ctx, const vattn_append_params* params, const int32_t* page_table,
                  const int32_t* seq_lens, int batch, void* stream);
 
@@ -347,6 +350,8 @@ int vattn_append(vattn_ctx* ctx, const vattn_append_params* params, const int32_
  * from 0 to batch, a prefix outside [0, max_ctx]) set VATTN_DEV_BAD_GROUP, and
  * a prefix page out of range VATTN_DEV_BAD_PAGE: the sequences of such a group,
  * and those in no group, give a zero output.
+ * q and the caches start at multiples of 16 bytes, the other arrays at multiples of
+ * their element's size (else VATTN_EINVAL).
  * Uses the context's workspace like the other decodes: order the calls of one
  * context. */
 int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const void* k_cache,

@@ -510,3 +510,32 @@ def test_append_reports_bad_lengths_of_sequences_without_new_tokens():
     for x in got[1:]:
         assert torch.equal(x["k_cache"], got[0]["k_cache"]) and torch.equal(x["v_cache"], got[0]["v_cache"])
     dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_refuses_pointers_between_elements(dtype):
+    c, max_ctx = _case(dtype=dtype, d=64, Hq=8, Hkv=2, ps=16, new=[3, 2], before=[2, 30], proxy="loki")
+    dec = _decoder(dtype, 64, 8, 2, 16, 2, max_ctx, "loki")
+    x = _cuda(c)
+    out = torch.zeros_like(x["q"])
+
+    def rc(table=0, lens=0, **off):
+        a = dict(k=x["k"], v=x["v"], q=x["q"], q_out=out, k_cache=x["k_cache"], v_cache=x["v_cache"],
+                 k_proj_cache=x["k_proj_cache"], proj_basis=x["proj_basis"], cu_tokens=x["cu_tokens"])
+        a = {k: t.data_ptr() + off.get(k, 0) for k, t in a.items()}
+        p = _abi.vattn_append_params(tokens=5, num_pages=x["num_pages"], k_stride=128, v_stride=128, q_stride=512, **a)
+        return _abi.vattn_append(dec.ctx, p, x["page_table"].data_ptr() + table, x["seq_lens"].data_ptr() + lens, 2,
+                                 check=False)
+
+    for name in ("k", "v", "q", "q_out"):
+        for off in ((1,) if dtype == "bf16" else (1, 2, 3)):
+            assert rc(**{name: off}) == _abi.VATTN_EINVAL, name
+    for name in ("table", "lens", "cu_tokens", "proj_basis"):
+        for off in (1, 2, 3):
+            assert rc(**{name: off}) == _abi.VATTN_EINVAL, name
+    for name in ("k_cache", "v_cache", "k_proj_cache"):
+        assert rc(**{name: 8}) == _abi.VATTN_EINVAL, name
+    assert torch.equal(x["k_cache"].cpu(), c["k_cache"]) and not out.any()
+    assert rc() == _abi.VATTN_OK and dec.last_error() == 0
+    dec.close()

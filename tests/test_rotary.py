@@ -71,6 +71,15 @@ def test_rotate_refusals_before_any_launch():
     assert _call(plan, heads=0, x=0, out=0, pos=0) == _abi.VATTN_OK
 
 
+def test_rotate_refuses_pointers_between_elements():
+    plan = Rotary(head_dim=128).plan
+    for dtype, off in ((_abi.VATTN_BF16, 1), (_abi.VATTN_FP32, 1), (_abi.VATTN_FP32, 2)):
+        for name, base in (("x", 1 << 20), ("out", 1 << 21)):
+            assert _call(plan, dtype=dtype, **{name: base + off}) == _abi.VATTN_EINVAL, (dtype, name, off)
+    for off in (1, 2, 3):
+        assert _call(plan, pos=(1 << 22) + off) == _abi.VATTN_EINVAL
+
+
 def test_rotate_wrapper_refuses_host_tensors_and_shapes():
     r = Rotary(head_dim=64)
     x = torch.zeros(3, 2, 64)

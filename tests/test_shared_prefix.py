@@ -320,6 +320,30 @@ def test_shared_output_at_any_float(dtype, kv_location):
     dec.close()
 
 
+@pytest.mark.gpu
+def test_shared_refuses_pointers_between_elements():
+    x = shared_batch([2], [20], [1, 2], Hq=8, Hkv=2, d=64, ps=16, dtype=torch.bfloat16)
+    dec = _decoder(x, "bf16", 16)
+    y = _cuda(x)
+    out = torch.full((2, 8, 64), 5.0, device="cuda")
+
+    def rc(**off):
+        a = dict(q=y["q"], k_cache=y["k_cache"], v_cache=y["v_cache"], page_table=y["page_table"],
+                 seq_lens=y["seq_lens"], group_start=y["group_start"], prefix_lens=y["prefix_lens"])
+        a = [t.data_ptr() + off.get(k, 0) for k, t in a.items()]
+        return _abi.vattn_shared_dense_decode(dec.ctx, *a, 1, 2, x["num_pages"], out.data_ptr() + off.get("out", 0),
+                                              check=False)
+
+    for name in ("page_table", "seq_lens", "group_start", "prefix_lens", "out"):
+        for off in (1, 2, 3):
+            assert rc(**{name: off}) == _abi.VATTN_EINVAL, name
+    for name in ("q", "k_cache", "v_cache"):
+        assert rc(**{name: 4}) == _abi.VATTN_EINVAL, name
+    assert (out == 5).all()
+    assert rc() == _abi.VATTN_OK and dec.last_error() == 0
+    dec.close()
+
+
 # ------------------------------------------------------------ as they are used together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -18,6 +18,7 @@
 namespace {
 
 using vattn::aligned16;
+using vattn::aligned_to;
 using vattn::Elem;
 
 constexpr int kThreads = 256;
@@ -804,6 +805,7 @@ int vattn_rotate(const vattn_rope* rope, const void* x, void* out, const int32_t
   if (dtype != VATTN_FP32 && dtype != VATTN_BF16) return VATTN_EINVAL;
   if (tokens == 0 || heads == 0) return VATTN_OK;
   if (!x || !out || !positions) return VATTN_EINVAL;
+  if (!aligned_to(dtype == VATTN_BF16 ? 2 : 4, x, out) || !aligned_to(4, positions)) return VATTN_EINVAL;
   const int D = rope->head_dim;
   if (xt < 0 || xh < 0 || ot < 0 || oh < 0) return VATTN_EINVAL;
   // no two rows of out overlap: heads within a token's span, or tokens within a head's
@@ -855,6 +857,9 @@ int vattn_append(vattn_ctx* ctx, const vattn_append_params* prm, const int32_t* 
   }
   if (!page_table || !seq_lens || !prm->k || !prm->v || !prm->k_cache || !prm->v_cache) return VATTN_EINVAL;
   if (prm->q && !prm->q_out) return VATTN_EINVAL;
+  if (!aligned_to(c.dtype == VATTN_BF16 ? 2 : 4, prm->k, prm->v, prm->q, prm->q_out) ||
+      !aligned_to(4, page_table, seq_lens, prm->cu_tokens, prm->proj_basis))
+    return VATTN_EINVAL;
   const long long kvw = static_cast<long long>(c.num_kv_heads) * D, qw = static_cast<long long>(c.num_q_heads) * D;
   if (prm->k_stride < kvw || prm->v_stride < kvw) return VATTN_EINVAL;
   if (prm->q && (prm->q_stride < qw || (prm->q == prm->q_out && prm->q_stride != qw))) return VATTN_EINVAL;

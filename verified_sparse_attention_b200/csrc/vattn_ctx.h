@@ -94,6 +94,11 @@ namespace vattn {
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Every one of the arrays starts at an element of `size` bytes (a null pointer does).
+template <typename... P>
+bool aligned_to(size_t size, const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) % size == 0) && ...);
+}
 
 // The driver's tensor-map encoder, reached through the runtime (the library
 // does not link the driver library itself).

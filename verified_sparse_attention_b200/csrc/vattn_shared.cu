@@ -166,6 +166,7 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
   if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !group_start || !prefix_lens || !out)
     return VATTN_EINVAL;
   if (!vattn::aligned16(q) || !vattn::aligned16(k_cache) || !vattn::aligned16(v_cache)) return VATTN_EINVAL;
+  if (!vattn::aligned_to(4, page_table, seq_lens, group_start, prefix_lens, out)) return VATTN_EINVAL;
   vattn::DeviceScope scope(ctx->device);
   if (!scope.ok) return ctx->last_status = VATTN_ECUDA;
   SharedParams P;
