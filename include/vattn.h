@@ -344,12 +344,14 @@ int vattn_append(vattn_ctx* ctx, const vattn_append_params* params, const int32_
  *                sequence of the group. They are read through the page table of
  *                the group's first sequence (which has to list them even if that
  *                sequence itself is shorter), the rest through each
- *                sequence's own. The prefix need not end on a page.
+ *                sequence's own, whose entries and rows for the prefix's
+ *                positions may hold anything. The prefix need not end on a page.
  * A sequence shorter than its group's prefix is decoded by itself from its own
  * pages. An empty sequence gives a zero output. Invalid groups (not ascending
- * from 0 to batch, a prefix outside [0, max_ctx]) set VATTN_DEV_BAD_GROUP, and
- * a prefix page out of range VATTN_DEV_BAD_PAGE: the sequences of such a group,
- * and those in no group, give a zero output.
+ * from 0 to batch, a prefix outside [0, max_ctx]) set VATTN_DEV_BAD_GROUP: the
+ * sequences of such a group, and those in no group, give a zero output. A page
+ * out of range sets VATTN_DEV_BAD_PAGE: the sequences that would read it give a
+ * zero output.
  * q and the caches start at multiples of 16 bytes, the other arrays at multiples of
  * their element's size (else VATTN_EINVAL).
  * Uses the context's workspace like the other decodes: order the calls of one

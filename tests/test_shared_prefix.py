@@ -344,6 +344,54 @@ def test_shared_refuses_pointers_between_elements():
     dec.close()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("unlisted", ["invalid", "stale"])
+@pytest.mark.parametrize("dtype,ps,kv_location", [("bf16", 16, "device"), ("bf16", 48, "device"), ("bf16", 2048, "device"),
+                                                  ("f32", 16, "device"), ("f32", 48, "device"), ("f32", 2048, "device"),
+                                                  ("f32", 16, "host"), ("bf16", 48, "host")])
+def test_shared_prefix_is_read_through_the_first_sequence(dtype, ps, kv_location, unlisted):
+    # one, two, three or all of a group reach the prefix's end, with the first and without it; only the first lists
+    # the prefix's pages, and the others' rows of the page that it ends in hold nothing of it
+    sizes, prefixes = [3, 2, 4, 3, 1, 6], [100, 57, 200, 64, 30, 90]
+    own = [-50, -100, 20, -10, 5, -3, 40, 0, -200, 0, 1, 33, 7, -1, 3, -90, 50, 16, 0]
+    x = shared_batch(sizes, prefixes, own, Hq=8, Hkv=2, d=64, ps=ps, dtype=DT[dtype], seed=4)
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    k, v, table = x["k_cache"].clone(), x["v_cache"].clone(), x["page_table"].clone()
+    used = torch.zeros(x["num_pages"], dtype=torch.bool)
+    used[table[table >= 0].long()] = True
+    stale = int((~used).nonzero()[0])                    # a page of garbage
+    start = x["group_start"].tolist()
+    for g, prefix in enumerate(prefixes):
+        for b in range(start[g] + 1, start[g + 1]):
+            if int(x["seq_lens"][b]) < prefix:
+                continue
+            whole, rest = divmod(prefix, ps)
+            table[b, :whole] = -1 if unlisted == "invalid" else stale
+            if rest and int(x["seq_lens"][b]) == prefix:
+                table[b, whole] = -1 if unlisted == "invalid" else stale
+            elif rest:
+                k[int(table[b, whole]), :, :rest] = float("nan")
+                v[int(table[b, whole]), :, :rest] = float("nan")
+    dec = _decoder(x, dtype, ps, kv_location=kv_location)
+    y = _cuda(dict(x, k_cache=k, v_cache=v, page_table=table))
+    if kv_location == "host":
+        y["k_cache"], y["v_cache"] = k.pin_memory(), v.pin_memory()
+    got = _call(dec, y).cpu().double()
+    assert dec.last_error() == 0
+    assert float((got - ref).abs().max()) <= _tol(x, 64)
+    # a first sequence that lists a bad page: those that read it give zeros and it is reported, the others (short of
+    # the prefix) are decoded from their own pages
+    for page in (-1, x["num_pages"]):
+        bad = y["page_table"].clone()
+        bad[start[2], 0] = page                          # group 2: sequences 5 (first, short), 6, 7, 8 (empty)
+        got = _call(dec, dict(y, page_table=bad)).cpu().double()
+        assert dec.last_error() == _abi.VATTN_DEV_BAD_PAGE
+        assert not got[[5, 6, 7, 8]].any()
+        rest = [b for b in range(len(own)) if not 5 <= b < 9]
+        assert float((got - ref)[rest].abs().max()) <= _tol(x, 64)
+    dec.close()
+
+
 # ------------------------------------------------------------ as they are used together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -517,7 +517,8 @@ __device__ __forceinline__ int tail_position(const int* topk, int k, int s1, int
 //           draws t in [p, b).
 //   dense:  part 0 = every position.
 // kModeSuffix: dense over positions [inf.s1, inf.n) (the part of a sequence
-// behind a shared prefix)
+// behind a shared prefix); those below inf.wst are read through the page-table
+// row of sequence inf.p
 constexpr int kModeDet = 0, kModeSample = 1, kModeDense = 2, kModeSuffix = 3;
 
 // Each warp streams its blocks of R rows through a private ring of NS
@@ -1542,6 +1543,7 @@ __global__ void __launch_bounds__(GatherShape<T, D, G>::NW * 32, 1) k_gather(con
       }
     const UnitInfo inf = P.info[u];
     const int pid_c = P.pps == 1 ? P.page_table[static_cast<size_t>(b) * P.pps] : 0;
+    const int pid_f = MODE == kModeSuffix && P.pps == 1 && inf.wst > 0 ? P.page_table[inf.p] : pid_c;
     const bool valid = inf.n > 0;
     const int* sel = P.sel + static_cast<size_t>(u) * P.max_ctx;
     const bool whole_tail = MODE == kModeSample && inf.mode == 2 && inf.exhausted;
@@ -1591,6 +1593,11 @@ __global__ void __launch_bounds__(GatherShape<T, D, G>::NW * 32, 1) k_gather(con
       return sel[i];
     };
     auto pid_of = [&](int pos) -> int {
+      if (MODE == kModeSuffix) {
+        const bool first = pos < inf.wst;
+        if (P.pps == 1) return first ? pid_f : pid_c;
+        return pos < 0 ? 0 : P.page_table[static_cast<size_t>(first ? inf.p : b) * P.pps + page_slot(P, pos)];
+      }
       if (P.pps == 1) return pid_c;
       return pos < 0 ? 0 : P.page_table[static_cast<size_t>(b) * P.pps + page_slot(P, pos)];
     };

@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       int g = 0;
       while (tail.start[g + 1] <= b) g++;
       const int prefix = tail.prefix[g];
-      if (prefix > 0 && prefix <= P.D.max_ctx && n >= prefix) atomicAdd(&tail.reach[g], 1);
+      if (prefix <= 0 || prefix > P.D.max_ctx) continue;
+      const int add = n >= prefix ? 1 : b == tail.start[g] ? kFirstShort : 0;
+      if (add) atomicAdd(&tail.reach[g], add);
     }
     __syncthreads();
     if (warp == 0) {  // lane g: group g; lane `groups`: the totals
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
         r.b0 = tail.start[lane];
         r.size = tail.start[lane + 1] - r.b0;
         r.prefix = tail.prefix[lane];
-        if (!bad && tail.reach[lane] >= P.min_reach) group_work(P, r, tiles, rows);
+        if (!bad && is_shared(P, tail.reach[lane])) group_work(P, r, tiles, rows);
       }
       long long it = tiles, ir = rows;
 #pragma unroll

@@ -16,7 +16,11 @@
 // row. Only groups of which min_reach sequences reach the end of the prefix are
 // shared: the others, and sequences shorter than their prefix, are left to
 // the own part whole, so that no row of a segment is masked and every key of a
-// tile counts for every row.
+// tile counts for every row. The prefix of a sequence that reaches its end is
+// read through the pages of the group's first sequence in every case: the
+// gather looks each position up in the one row or the other; k_shared_own reads
+// one row per sequence, so for it a single sequence behind a first one that is
+// shorter makes a group shared.
 #pragma once
 
 #include "vattn_ctx.h"
@@ -41,7 +45,7 @@ struct SharedParams {
   int RB, KT;  // rows of a block, keys of a tile
   int box;     // rows of a cache box: a power of two that divides the page size, at most KT
   int own_warps;  // k_shared_own's warps; 0: the gather takes the own positions
-  int min_reach;  // sequences that have to reach a prefix's end for it to be shared, at least 2
+  int min_reach;  // sequences that have to reach a prefix's end for it to be shared, at least 2 (but see is_shared)
 };
 
 // ---------------------------------------------------------------- groups
@@ -58,6 +62,14 @@ __device__ __forceinline__ void group_work(const SharedParams& P, SharedGroup& g
   g.tiles = (g.prefix + P.KT - 1) / P.KT;
   tiles = static_cast<long long>(g.tiles) * ((nrow + P.RB - 1) / P.RB) * P.D.Hkv;
   rows = static_cast<long long>(nrow) * P.D.Hkv;
+}
+
+// How far a group's sequences reach: a count of those that reach the prefix's
+// end, plus kFirstShort if the first sequence does not.
+constexpr int kFirstShort = 1 << 30;
+__device__ __forceinline__ bool is_shared(const SharedParams& P, int reach) {
+  const int cnt = reach & (kFirstShort - 1);
+  return cnt >= P.min_reach || (P.own_warps > 0 && cnt > 0 && cnt != reach);
 }
 
 // Chunks of k_shared_own that cover positions [start, n): kOwnChunk positions
@@ -99,12 +111,14 @@ __device__ __forceinline__ bool bad_pages(const SharedParams& P, int b, int s0, 
   return __any_sync(0xffffffffu, bad);
 }
 
-// Sequences of [b0, b1) that reach position `prefix` (a warp).
+// How far the sequences [b0, b1) reach with a prefix of `prefix` (a warp).
 __device__ __forceinline__ int count_reach(const SharedParams& P, int b0, int b1, int prefix) {
   int cnt = 0;
   for (int base = b0; base < b1; base += 32) {
     const int b = base + (threadIdx.x & 31);
-    cnt += __popc(__ballot_sync(0xffffffffu, b < b1 && prefix > 0 && checked_len(P, b) >= prefix));
+    const unsigned reach = __ballot_sync(0xffffffffu, b < b1 && prefix > 0 && checked_len(P, b) >= prefix);
+    if (base == b0 && prefix > 0 && !(reach & 1u)) cnt = kFirstShort;
+    cnt += __popc(reach);
   }
   return cnt;
 }
@@ -152,7 +166,9 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
     for (int o = 16; o; o >>= 1) own = max(own, __shfl_xor_sync(0xffffffffu, own, o));
     if (job < D.batch) {
       const int b = job, g = own;
-      int n = checked_len(P, b), start = 0;
+      // positions [0, start) are left to the prefix kernel, [start, first) are read
+      // through the pages of the group's first sequence b0, the rest through its own
+      int n = checked_len(P, b), start = 0, first = 0, b0 = 0;
       if (lane == 0 && n < 0) atomicOr(D.err, kDevBadSeqlen);
       if (n < 0 || bad_bounds || g < 0) n = 0;
       if (n > 0) {
@@ -160,11 +176,14 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
         if (prefix < 0 || prefix > D.max_ctx) {
           n = 0;
         } else if (n >= prefix && prefix > 0) {
-          if (count_reach(P, P.group_start[g], P.group_start[g + 1], prefix) >= P.min_reach) start = prefix;
+          b0 = P.group_start[g];
+          if (is_shared(P, count_reach(P, b0, P.group_start[g + 1], prefix))) start = prefix;
+          else if (b != b0) first = prefix;
         }
       }
-      // only the positions behind the prefix are read through this row
-      if (n > start && bad_pages(P, b, start / D.ps, (n + D.ps - 1) / D.ps)) {
+      const int own0 = max(start, first);
+      if ((n > own0 && bad_pages(P, b, own0 / D.ps, (n + D.ps - 1) / D.ps)) ||
+          (n > 0 && first > 0 && bad_pages(P, b0, 0, (first + D.ps - 1) / D.ps))) {
         if (lane == 0) atomicOr(D.err, kDevBadPage);
         n = 0;
       }
@@ -172,7 +191,9 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
         UnitInfo inf = {};
         inf.n = n;
         inf.s1 = start;
+        inf.wst = first;
         inf.k = g;
+        inf.p = b0;
         D.info[static_cast<size_t>(b) * D.Hkv + h] = inf;
       }
       return;
@@ -185,7 +206,7 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
         if (lane == 0) atomicOr(D.err, kDevBadGroup);
       } else {
         ok = 1;
-        if (count_reach(P, b0, b1, prefix) >= P.min_reach && bad_pages(P, b0, 0, (prefix + D.ps - 1) / D.ps)) {
+        if (is_shared(P, count_reach(P, b0, b1, prefix)) && bad_pages(P, b0, 0, (prefix + D.ps - 1) / D.ps)) {
           if (lane == 0) atomicOr(D.err, kDevBadPage);
           ok = 0;
         }
@@ -240,8 +261,9 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
   if (!bad_bounds) {
     for (int b = tid; b < D.batch; b += blockDim.x) {
       const int g = group_of(b), prefix = prefix_of(g);
-      if (prefix > 0 && prefix <= D.max_ctx && len(b) >= prefix)
-        atomicAdd(g < kSharedPrepKeep ? &s_reach[g] : &g_reach[g], 1);
+      if (prefix <= 0 || prefix > D.max_ctx) continue;
+      const int add = len(b) >= prefix ? 1 : b == start_of(g) ? kFirstShort : 0;
+      if (add) atomicAdd(g < kSharedPrepKeep ? &s_reach[g] : &g_reach[g], add);
     }
   }
   __threadfence_block();
@@ -257,7 +279,7 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
         rec.b0 = start_of(g);
         rec.size = start_of(g + 1) - rec.b0;
         rec.prefix = prefix_of(g);
-        if (reach_of(g) >= P.min_reach) group_work(P, rec, t, r);
+        if (is_shared(P, reach_of(g))) group_work(P, rec, t, r);
       }
       const long long it = block_scan_ll(t, s_w), ir = block_scan_ll(r, s_w);
       if (g < P.groups) {
@@ -288,7 +310,7 @@ static __global__ void __launch_bounds__(kSharedPrepThreads) k_shared_prep(const
     if (b >= D.batch || bad_bounds) return -1;
     const int g = group_of(b), n = len(b), prefix = prefix_of(g);
     if (n <= 0 || prefix < 0 || prefix > D.max_ctx) return -1;
-    return prefix > 0 && n >= prefix && reach_of(g) >= P.min_reach ? prefix : 0;
+    return prefix > 0 && n >= prefix && is_shared(P, reach_of(g)) ? prefix : 0;
   };
   if (P.own_warps) {
     long long sum = 0;  // chunks of one KV head
