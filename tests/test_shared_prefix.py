@@ -392,6 +392,25 @@ def test_shared_prefix_is_read_through_the_first_sequence(dtype, ps, kv_location
     dec.close()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_shared_scores_far_below_zero(dtype, prefix):
+    # every key has the same score, about -1.6e32 (exact: one product of powers of two): the mean of the values
+    x = shared_batch([6], [prefix], [5, 1, 40, 17, 9, 3], Hq=8, Hkv=2, d=64, ps=16, dtype=DT[dtype], seed=6)
+    x["q"] = torch.zeros_like(x["q"])
+    x["q"][..., 3] = 2.0**60
+    k = torch.zeros_like(x["k_cache"])
+    k[..., 3] = -2.0**50
+    x["k_cache"] = torch.where(x["k_cache"].isnan(), x["k_cache"], k)
+    dec = _decoder(x, dtype, 16)
+    got = _call(dec, _cuda(x)).cpu().double()
+    assert dec.last_error() == 0
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    assert float((got - ref).abs().max()) <= _tol(x, 64)
+    dec.close()
+
+
 # ------------------------------------------------------------ as they are used together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
           }
           top *= c;
           if (i <= 0) {
-            m = fmaxf(top, -1e30f);  // finite: scores of -inf weigh exactly 0
+            m = fmaxf(top, kLowest);
           } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
             const float mn = top > m + kRescale ? top : m;
             const float f = ex2(m - mn);
@@ -574,8 +574,11 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
               unsigned w[32];  // hi terms, then lo terms
 #pragma unroll
               for (int j = 0; j < 16; j++) {
-                const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[k][2 * j]), __uint_as_float(x[k][2 * j + 1])),
-                                            make_float2(c, c), make_float2(neg, neg));
+                // (product and difference rounded apart, as the maximum's product is: fused, scores of
+                // 2^31 and more would leave their own maximum by more than fp32's range of exponents)
+                const float2 y = __fadd2_rn(
+                    __fmul2_rn(make_float2(__uint_as_float(x[k][2 * j]), __uint_as_float(x[k][2 * j + 1])), make_float2(c, c)),
+                    make_float2(neg, neg));
                 const float2 p = make_float2(ex2(y.x), ex2(y.y));
                 sum = __fadd2_rn(sum, p);
                 w[j] = pack_bf16x2(p.x, p.y);

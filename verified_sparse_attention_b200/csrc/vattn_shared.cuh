@@ -72,6 +72,10 @@ __device__ __forceinline__ bool is_shared(const SharedParams& P, int reach) {
   return cnt >= P.min_reach || (P.own_warps > 0 && cnt > 0 && cnt != reach);
 }
 
+// The running maxima start here: finite, so that scores of -inf weigh exactly 0,
+// and below every finite score.
+constexpr float kLowest = -3.402823466e38f;
+
 // Chunks of k_shared_own that cover positions [start, n): kOwnChunk positions
 // each from the 16-position block that holds `start`. Warps take them in pieces
 // of at least kOwnPiece chunks of one (sequence, KV head), about kOwnPieces a
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(256, 1) k_shared_prefix(const __grid_constant_
         }
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const float mn = fmaxf(fmaxf(m[i], mx), -1e30f);  // finite: scores of -inf weigh exactly 0
+        const float mn = fmaxf(fmaxf(m[i], mx), kLowest);
         const float f = exp2f(m[i] - mn);
         m[i] = mn;
         float sum = 0.0f;
@@ -859,7 +863,7 @@ __global__ void __launch_bounds__(OwnShape<D>::THREADS, 1) k_shared_own(const __
           float f[2];
 #pragma unroll
           for (int k = 0; k < 2; k++) {
-            const float nm = fmaxf(fmaxf(m[k], bm[k]), -1e30f);  // finite: scores of -inf weigh exactly 0
+            const float nm = fmaxf(fmaxf(m[k], bm[k]), kLowest);
             f[k] = exp2f(m[k] - nm);
             m[k] = nm;
             l[k] *= f[k];
