@@ -411,6 +411,131 @@ def test_shared_scores_far_below_zero(dtype, prefix):
     dec.close()
 
 
+# ------------------------------------------------------------ precision
+def _row_errors(got, ref):
+    """|got - ref| of every row over the row's norm (rows that are not zero)."""
+    norm = ref.norm(dim=-1)
+    return ((got - ref).norm(dim=-1) / norm)[norm > 0]
+
+
+# For random values the error of a row is at most the weights' relative error times the row's norm, as the errors of
+# different keys do not add up. A weight of the bf16 kernels is two bf16 terms, 2^-8 of 2^-8 off at most (1.5e-5); the
+# tensor core's truncation takes up to 7e-6 from every component; fp32 scores, exponentials and sums are a few 1e-6 off.
+# A second term left out is 1e-3, a key of 20001 left out 7e-3, a tile of 128 keys in 130000 3e-2.
+ROW_TOL = 4e-5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sizes,prefixes,ps", [([5], [300], 16), ([3, 8, 1, 6], [1000, 129, 40, 513], 48),
+                                               ([40], [700], 128), ([70, 10], [400, 128], 64), ([6, 10], [20001, 9000], 16),
+                                               ([2] * 20, [100] * 20, 16)])
+def test_shared_rows_are_precise(dtype, d, sizes, prefixes, ps):
+    B = sum(sizes)
+    x = shared_batch(sizes, prefixes, [(37 * b) % 150 for b in range(B)], Hq=8, Hkv=2, d=d, ps=ps, dtype=DT[dtype], seed=8)
+    dec = _decoder(x, dtype, ps)
+    got = _call(dec, _cuda(x)).cpu().double()
+    assert dec.last_error() == 0
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    assert float(_row_errors(got, ref).max()) <= ROW_TOL
+    dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [6, 50])
+def test_shared_constant_values_come_back(dtype, d, B):
+    # the weights' sum has to be that of the terms that meet the values: what each weight loses shows undiminished,
+    # here with few keys that count (queries four times as long)
+    x = shared_batch([B], [700], [(3 * b) % 60 for b in range(B)], Hq=8, Hkv=2, d=d, ps=16, dtype=DT[dtype], seed=9)
+    x["q"] = x["q"] * 4
+    value = 0.7109375
+    x["v_cache"] = torch.where(x["v_cache"].isnan(), x["v_cache"], torch.full_like(x["v_cache"], value))
+    dec = _decoder(x, dtype, 16)
+    got = _call(dec, _cuda(x)).cpu().double()
+    assert dec.last_error() == 0
+    # 2^-16 of a weight, the truncation of six tiles' products and fp32 sums of 760 terms
+    assert float((got / value - 1).abs().max()) <= 2**-15
+    dec.close()
+
+
+def _uniform_batch(B, heads, prefix, own, scale, *, d=64, ps=1024, seed=5):
+    """bf16 sequences of equal length over one prefix in whole pages, on the GPU; keys of position p times scale(p)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    whole, more = prefix // ps, -(-own // ps)
+    pages = whole + B * more
+    k, v = (torch.empty(pages, heads, ps, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for c in (k, v):
+        for p in range(0, pages, 64):
+            c[p:p + 64] = torch.randn(c[p:p + 64].shape, generator=g, device="cuda").bfloat16()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.cat([torch.arange(whole, **i32).expand(B, whole),
+                       whole + torch.arange(B * more, **i32).view(B, more)], 1).contiguous()
+    for b in range(B) if own else range(1):
+        first = 0 if b == 0 else whole
+        for slot in range(first, whole + more):
+            pos = slot * ps + torch.arange(ps, device="cuda")
+            page = int(table[b, slot])
+            k[page] = (k[page].float() * scale(pos.float())[:, None]).bfloat16()
+    return dict(q=torch.randn(B, heads, d, generator=g, device="cuda").bfloat16(), k_cache=k, v_cache=v, page_table=table,
+                seq_lens=torch.full((B,), prefix + own, **i32), group_start=torch.tensor([0, B], **i32),
+                prefix_lens=torch.tensor([prefix], **i32), num_pages=pages, max_ctx=(whole + more) * ps)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,heads,prefix,own,period", [
+    (3, 16, 102400, 5, 102400), (140, 16, 40960, 3, 40960), (2, 2, 130048, 1, 130048),  # long prefixes
+    (64, 8, 0, 8000, 656),    # own parts of more chunks than one accumulator takes (64 * 500 * 8 over 6 * 1036 places)
+    (32, 8, 4096, 16000, 700)])
+def test_shared_long_parts_are_precise(B, heads, prefix, own, period):
+    # scores that rise along every period, so that the maximum moves behind the first accumulators
+    x = _uniform_batch(B, heads, prefix, own, lambda pos: 0.5 + 1.5 * (pos % period) / period)
+    dec = _decoder(x, "bf16", 1024)
+    got = _call(dec, x).double()
+    assert dec.last_error() == 0
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    assert float(_row_errors(got, ref).max()) <= ROW_TOL
+    x["v_cache"].fill_(0.7109375)
+    got = _call(dec, x).double() / 0.7109375
+    assert float((got - 1).abs().max()) <= 2**-15
+    dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_captured_call_follows_new_groups(dtype):
+    x = shared_batch([6, 5], [300, 130], [(5 * b) % 20 for b in range(11)], Hq=8, Hkv=2, d=64, ps=16, dtype=DT[dtype])
+    dec = _decoder(x, dtype, 16)
+    y = _cuda(x)
+    out = torch.zeros(11, 8, 64, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _call(dec, y, out=out)
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    # other groups over the same contents: shorter prefixes, one more sequence or fewer in the first group, no prefix
+    for start, prefixes in (([0, 6, 11], [300, 130]), ([0, 6, 11], [77, 130]), ([0, 3, 11], [300, 0]),
+                            ([0, 0, 11], [40, 0]), ([0, 5, 11], [299, 0])):
+        y["group_start"].copy_(torch.tensor(start, dtype=torch.int32))
+        y["prefix_lens"].copy_(torch.tensor(prefixes, dtype=torch.int32))
+        out.fill_(float("nan"))
+        graph.replay()
+        assert float(_row_errors(out.cpu().double(), ref).max()) <= ROW_TOL, (start, prefixes)
+        assert dec.last_error() == 0
+    # lengths too: two sequences of the first group end before its prefix
+    lens = x["seq_lens"].clone()
+    lens[1], lens[4] = 20, 0
+    y["seq_lens"].copy_(lens)
+    y["group_start"].copy_(x["group_start"])
+    y["prefix_lens"].copy_(x["prefix_lens"])
+    graph.replay()
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], lens)
+    assert float(_row_errors(out.cpu().double(), ref).max()) <= ROW_TOL and not out[4].any()
+    assert dec.last_error() == 0
+    dec.close()
+
+
 # ------------------------------------------------------------ as they are used together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
