@@ -64,6 +64,16 @@ def test_append_needs_a_context():
         _fake().append(**_args())
 
 
+def test_append_wrapper_takes_views_of_a_single_token():
+    # a row of a wider tensor is contiguous: as q_out, and in place
+    wide = torch.zeros(1, 12, 64, dtype=torch.bfloat16)
+    one = dict(k=wide[:, 8:10], v=wide[:, 10:], page_table=torch.zeros(1, 7, dtype=torch.int32),
+               seq_lens=torch.ones(1, dtype=torch.int32), q=wide[:, :8])
+    for out in (None, wide[:, :8], torch.zeros(1, 9, 64, dtype=torch.bfloat16)[:, 1:]):
+        with pytest.raises(_abi.VattnError):   # everything in order but the context
+            _fake().append(**_args(**one, q_out=out))
+
+
 # ------------------------------------------------------------ on the GPU
 def _case(*, dtype, d, Hq, Hkv, ps, new, before, proxy, seed=0, wide=False, pad=0, spare=1):
     """One call's tensors: sequence b has before[b] positions and gets new[b] (host tensors)."""
@@ -538,4 +548,24 @@ def test_append_refuses_pointers_between_elements(dtype):
         assert rc(**{name: 8}) == _abi.VATTN_EINVAL, name
     assert torch.equal(x["k_cache"].cpu(), c["k_cache"]) and not out.any()
     assert rc() == _abi.VATTN_OK and dec.last_error() == 0
+    dec.close()
+
+
+@pytest.mark.gpu
+def test_append_one_token_of_a_wide_row_in_place():
+    c, max_ctx = _case(dtype="bf16", d=64, Hq=8, Hkv=2, ps=16, new=[1], before=[20], proxy="exact", wide=True)
+    dec = _decoder("bf16", 64, 8, 2, 16, 1, max_ctx, "exact")
+    rotary = Rotary(head_dim=64)
+    x = _cuda(c)
+    want = dec.append(x["k"], x["v"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"], x["num_pages"],
+                      rotary=rotary, q=x["q"])
+    y = _cuda(c)
+    wide = torch.cat([c["q"], c["k"], c["v"], c["v"][:, :1]], 1).cuda()
+    keep = wide.clone()
+    q = wide[:, :8]
+    assert dec.append(wide[:, 8:10], wide[:, 10:12], y["k_cache"], y["v_cache"], y["page_table"], y["seq_lens"],
+                      y["num_pages"], rotary=rotary, q=q, q_out=q) is q
+    assert dec.last_error() == 0
+    assert torch.equal(q, want) and torch.equal(wide[:, 8:], keep[:, 8:])
+    assert torch.equal(y["k_cache"], x["k_cache"]) and torch.equal(y["v_cache"], x["v_cache"])
     dec.close()

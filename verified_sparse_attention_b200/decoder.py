@@ -111,8 +111,8 @@ class SparseDecoder:
                 or (heads > 1 and t.stride(1) != self.head_dim) or t.get_device() != self._index:
             raise ValueError(f"{name} must be {self.dtype} [{tokens}, {heads}, {self.head_dim}] on {self.device} with "
                              "the heads of a token contiguous")
-        # a single token's stride says nothing
-        return max(t.stride(0), heads * self.head_dim) if tokens <= 1 else t.stride(0)
+        # a single token's stride says nothing: its row is contiguous, a view of a wider one too
+        return heads * self.head_dim if tokens <= 1 else t.stride(0)
 
     def append(self, k, v, k_cache, v_cache, page_table, seq_lens, num_pages, *, cu_tokens=None, rotary=None, q=None,
                q_out=None, k_t_cache=None, k_proj_cache=None, proj_basis=None, stream=None):
