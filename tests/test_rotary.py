@@ -1,4 +1,5 @@
 """Rotary positions: the plan (CPU) and vattn_rotate against 64-bit rotations (GPU)."""
+import ctypes as C
 import math
 
 import pytest
@@ -6,6 +7,7 @@ import torch
 
 from tests.serving import amplitude, frequencies, rotate64
 from verified_sparse_attention_b200 import _abi
+from verified_sparse_attention_b200.decoder import SparseDecoder
 from verified_sparse_attention_b200.rotary import Rotary
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -195,3 +197,33 @@ def test_rotate_on_another_stream_and_captured():
     pos += 3
     graph.replay()
     assert torch.equal(out, r.rotate(x, pos))
+
+
+@pytest.mark.gpu
+def test_rotate_failure_leaves_nothing_for_the_next_call():
+    # a stream whose capture was spoiled (by waiting for it on the host) refuses launches
+    rt = C.CDLL("libcudart.so.12")
+    stream, graph = C.c_void_p(), C.c_void_p()
+    x = torch.randn(5, 4, 64, device="cuda").bfloat16()
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    r = Rotary(head_dim=64)
+    ref = r.rotate(x, pos)
+    dec = SparseDecoder(num_q_heads=4, num_kv_heads=4, head_dim=64, dtype=torch.bfloat16, page_size=16, max_batch=1,
+                        max_ctx=16)
+    cache = torch.randn(1, 4, 16, 64, device="cuda").bfloat16()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, lens = torch.zeros(1, 1, **i32), torch.full((1,), 9, **i32)
+    torch.cuda.synchronize()
+    assert rt.cudaStreamCreateWithFlags(C.byref(stream), 1) == 0
+    assert rt.cudaStreamBeginCapture(stream, 2) == 0
+    try:
+        assert rt.cudaStreamSynchronize(stream) != 0
+        with pytest.raises(_abi.VattnError):
+            r.rotate(x, pos, stream=stream.value)
+    finally:
+        rt.cudaStreamEndCapture(stream, C.byref(graph))
+        rt.cudaGetLastError()
+        rt.cudaStreamDestroy(stream)
+    dec.dense(x[:1], cache, cache, table, lens, 1)       # reported the failure of the rotation
+    assert dec.last_error() == 0 and torch.equal(r.rotate(x, pos), ref)
+    dec.close()

@@ -687,7 +687,9 @@ int launch_rows(void (*kern)(A), unsigned gx, unsigned gy, const A& a, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? VATTN_OK : VATTN_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess) return VATTN_OK;
+  cudaGetLastError();  // reported here: the next call's check must not find it
+  return VATTN_ECUDA;
 }
 
 template <typename T, int D>
@@ -814,8 +816,10 @@ int vattn_rotate(const vattn_rope* rope, const void* x, void* out, const int32_t
   if (x == out && ((tokens > 1 && xt != ot) || (heads > 1 && xh != oh))) return VATTN_EINVAL;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
     return VATTN_ECUDA;
+  }
   RotateArgs a;
   a.rope = *rope;
   a.x = x;
