@@ -20,7 +20,7 @@ struct SharedKernels {
   void (*own)(SharedParams);  // the sequences' own positions; nullptr: by the gather
   int own_nw;                 // its warps per CTA (one CTA per SM)
   size_t own_smem;
-  void (*gather)(DevParams);
+  void (*gather)(DevParams);  // where there is no own kernel
   unsigned gather_threads;
   size_t gather_smem;
   void (*combine[4])(SharedParams);  // 1, 2, 4 or 8 warps per row
@@ -29,29 +29,31 @@ struct SharedKernels {
 template <typename T, int D, int G>
 SharedKernels kernels_for(bool host_kv) {
   using vattn::kModeSuffix;
-  SharedKernels k;
-  k.prefix = host_kv ? vattn::k_shared_prefix<T, D, true> : vattn::k_shared_prefix<T, D, false>;
-  k.RB = vattn::PrefixShape<D>::RB;
-  k.KT = vattn::PrefixShape<D>::KT;
-  k.tc = false;
-  k.threads = 256;
-  k.smem = vattn::PrefixShape<D>::SMEM;
-  k.own = nullptr;
-  k.gather = host_kv ? vattn::k_gather<T, D, G, kModeSuffix, true> : vattn::k_gather<T, D, G, kModeSuffix>;
-  k.gather_smem = vattn::GatherShape<T, D, G>::SMEM;
-  k.gather_threads = vattn::GatherShape<T, D, G>::NW * 32;
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    if (!host_kv) {
-      k.prefix = vattn::k_shared_prefix_tc<D>;
-      k.RB = 2 * vattn::PrefixTcShape<D>::M;
-      k.KT = vattn::PrefixTcShape<D>::KT;
-      k.tc = true;
-      k.threads = vattn::PrefixTcShape<D>::THREADS;
-      k.smem = vattn::PrefixTcShape<D>::SMEM;
-      k.own = vattn::k_shared_own<D, G>;
-      k.own_nw = vattn::OwnShape<D>::NW;
-      k.own_smem = vattn::OwnShape<D>::SMEM;
-    }
+  SharedKernels k = {};
+  auto simt = [&](void (*prefix)(SharedParams), void (*gather)(DevParams)) {
+    k.prefix = prefix;
+    k.RB = vattn::PrefixShape<D>::RB;
+    k.KT = vattn::PrefixShape<D>::KT;
+    k.threads = 256;
+    k.smem = vattn::PrefixShape<D>::SMEM;
+    k.gather = gather;
+    k.gather_smem = vattn::GatherShape<T, D, G>::SMEM;
+    k.gather_threads = vattn::GatherShape<T, D, G>::NW * 32;
+  };
+  if (host_kv) {
+    simt(vattn::k_shared_prefix<T, D, true>, vattn::k_gather<T, D, G, kModeSuffix, true>);
+  } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    k.prefix = vattn::k_shared_prefix_tc<D>;
+    k.RB = 2 * vattn::PrefixTcShape<D>::M;
+    k.KT = vattn::PrefixTcShape<D>::KT;
+    k.tc = true;
+    k.threads = vattn::PrefixTcShape<D>::THREADS;
+    k.smem = vattn::PrefixTcShape<D>::SMEM;
+    k.own = vattn::k_shared_own<D, G>;
+    k.own_nw = vattn::OwnShape<D>::NW;
+    k.own_smem = vattn::OwnShape<D>::SMEM;
+  } else {
+    simt(vattn::k_shared_prefix<T, D, false>, vattn::k_gather<T, D, G, kModeSuffix>);
   }
   k.combine[0] = vattn::k_shared_combine<D, 1>;
   k.combine[1] = vattn::k_shared_combine<D, 2>;
@@ -143,7 +145,8 @@ size_t shared_workspace(vattn_ctx* ctx, char* p) {
     w.grid = ctx->num_sms;
     cudaFuncSetAttribute(k.prefix, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.smem));
     if (k.own) cudaFuncSetAttribute(k.own, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.own_smem));
-    cudaFuncSetAttribute(k.gather, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.gather_smem));
+    if (k.gather)
+      cudaFuncSetAttribute(k.gather, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.gather_smem));
   }
   return 3 * sz_int + sz_pre + 256 + sz_piece + sz_group + sz_rec + sz_ml + sz_orec + sz_oml;
 }
