@@ -536,6 +536,57 @@ def test_shared_captured_call_follows_new_groups(dtype):
     dec.close()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_sparse_and_dense_decodes_of_one_context(dtype):
+    # they have the same workspace, one after the other, whatever each leaves there
+    x = shared_batch([7, 5], [900, 400], [(41 * b) % 300 for b in range(12)], Hq=8, Hkv=2, d=64, ps=16, dtype=DT[dtype],
+                     seed=12, garbage=0.0)
+    y = _cuda(x)
+    bad = dict(y, q=torch.full_like(y["q"], float("nan")))
+    params = SparseDecoder.make_params(sinks=4, window=16, topk_abs=40, pilot_min=32, eps=0.05, delta=0.1, seed=3,
+                                       num_pages=x["num_pages"])
+
+    def caches(z):
+        return z["q"], z["k_cache"], z["v_cache"], z["page_table"], z["seq_lens"]
+
+    def sparse(dec, z):
+        res = dec.decode(*caches(z), params)
+        n = torch.arange(x["max_ctx"], device="cuda") < res["sel_count"][..., None]
+        return [res["out"], torch.where(n, res["sel_idx"], -1), res["sel_count"], res["budgets"], res["head_need"]]
+
+    calls = [sparse, lambda dec, z: [_call(dec, z)], lambda dec, z: [dec.dense(*caches(z), x["num_pages"])]]
+    want = []
+    for call in calls:
+        dec = _decoder(x, dtype, 16)
+        want.append(call(dec, y))
+        dec.close()
+    dec = _decoder(x, dtype, 16)
+    for order in ([0, 1, 2], [2, 1, 0], [1, 0, 1, 2, 0, 2, 1]):
+        for i in order:
+            assert all(torch.equal(a, b) for a, b in zip(calls[i](dec, y), want[i])), (order, i)
+        for i in order:                     # what follows is not to see what these leave
+            calls[i](dec, bad)
+    for i in (0, 1, 2, 1, 0):
+        assert all(torch.equal(a, b) for a, b in zip(calls[i](dec, y), want[i])), i
+    assert dec.last_error() == 0
+    dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,max_ctx", [(1, 32768), (64, 32768), (4096, 2048)])
+def test_shared_records_take_no_more_than_the_sparse_decodes_scratch(dtype, batch, max_ctx):
+    # keys and scores, 4 (1 + G) bytes per unit and position, and under 10 KB per unit and 16 MB of records and state
+    # for the rest; the shared prefixes' records (about 17 to 166 MB) are within the former or nearly so
+    Hq, Hkv = 32, 8
+    dec = SparseDecoder(num_q_heads=Hq, num_kv_heads=Hkv, head_dim=128, dtype=DT[dtype], page_size=16, max_batch=batch,
+                        max_ctx=max_ctx)
+    units = batch * Hkv
+    assert _abi.vattn_workspace_bytes(dec.ctx) <= units * max_ctx * 4 * (1 + Hq // Hkv) + units * 20480 + (16 << 20)
+    dec.close()
+
+
 # ------------------------------------------------------------ as they are used together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -230,9 +230,12 @@ int vattn_create(vattn_ctx** out, const vattn_config* cfg) {
   const size_t sz_rdet = align256((ctx->CD + 2 * U) * REC * sizeof(float));
   const size_t sz_rsmp = align256((ctx->CS + 2 * U) * REC * sizeof(float));
   const size_t sz_err = 256;
-  const size_t sz_shared = vattn::shared_workspace(ctx, nullptr);
-  ctx->ws_bytes = sz_info + 3 * sz_vec + sz_ordk + sz_hist + sz_ps + sz_nneed + sz_pre + sz_gcnt +
-                  2 * sz_spre + sz_rdet + sz_rsmp + sz_err + sz_shared;
+  // The sparse decode's keys, scores and sample records and the shared-prefix
+  // decode's records take the same place: no call reads what another left there,
+  // and the calls of a context are in order.
+  const size_t sz_scratch = std::max(sz_ordk + sz_ps + sz_rsmp, vattn::shared_workspace(ctx, nullptr));
+  ctx->ws_bytes = sz_info + 3 * sz_vec + sz_hist + sz_nneed + sz_pre + sz_gcnt + 2 * sz_spre + sz_rdet + sz_err +
+                  sz_scratch;
   if (cudaMalloc(&ctx->ws, ctx->ws_bytes) != cudaSuccess) {
     cudaGetLastError();
     delete ctx;
@@ -243,18 +246,18 @@ int vattn_create(vattn_ctx** out, const vattn_config* cfg) {
   ctx->qbar = reinterpret_cast<float*>(p); p += sz_vec;
   ctx->qsel = reinterpret_cast<float*>(p); p += sz_vec;
   ctx->dims = reinterpret_cast<int*>(p); p += sz_vec;
-  ctx->ordk = reinterpret_cast<unsigned*>(p); p += sz_ordk;
   ctx->hist = reinterpret_cast<unsigned*>(p); p += sz_hist;
-  ctx->pscore = reinterpret_cast<float*>(p); p += sz_ps;
   ctx->num_need = reinterpret_cast<int*>(p); p += sz_nneed;
   ctx->prefix = reinterpret_cast<long long*>(p); p += sz_pre;
   ctx->gcnt = reinterpret_cast<unsigned*>(p); p += sz_gcnt;
   ctx->pre_det = reinterpret_cast<long long*>(p); p += sz_spre;
   ctx->pre_samp = reinterpret_cast<long long*>(p); p += sz_spre;
   ctx->rec_det = reinterpret_cast<float*>(p); p += sz_rdet;
-  ctx->rec_samp = reinterpret_cast<float*>(p); p += sz_rsmp;
   ctx->err = reinterpret_cast<unsigned*>(p); p += sz_err;
   vattn::shared_workspace(ctx, p);
+  ctx->ordk = reinterpret_cast<unsigned*>(p); p += sz_ordk;
+  ctx->pscore = reinterpret_cast<float*>(p); p += sz_ps;
+  ctx->rec_samp = reinterpret_cast<float*>(p);
   if (cudaMemset(ctx->ws, 0, ctx->ws_bytes) != cudaSuccess) {
     cudaFree(ctx->ws);
     delete ctx;

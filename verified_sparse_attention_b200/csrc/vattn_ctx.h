@@ -31,6 +31,7 @@ struct SharedWork {
   int* reach = nullptr;           // [2 max_batch] scratch of k_shared_prep's last two CTAs
   int* pages_ok = nullptr;        // [max_batch] per group: the prefix's pages are valid
   SharedGroup* group = nullptr;   // [max_batch + 1]
+  int stride = 0;                 // record rows of a CTA of the prefix kernel
   float* rec = nullptr;           // [record rows][D]
   float2* ml = nullptr;           // [record rows] (maximum in log2 units, weight sum)
   int* own_pre = nullptr;         // [max_batch + 1] prefix sum of own pieces (of one KV head) over sequences
@@ -238,8 +239,8 @@ inline int finish(vattn_ctx* ctx, int launches) {
   return ctx->last_status;
 }
 
-// Bytes of the shared-prefix decode's part of the workspace, set out from `p`
-// when given (vattn_shared.cu).
+// Bytes of the shared-prefix decode's scratch, set out from `p` when given
+// (vattn_shared.cu). Nothing in it is kept from one call to the next.
 size_t shared_workspace(vattn_ctx* ctx, char* p);
 
 // The given device current for the lifetime of the object, whichever was before.

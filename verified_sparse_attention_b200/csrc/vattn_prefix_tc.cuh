@@ -485,8 +485,9 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
       const int valid = two ? s.rows - st * 128 : s.rows;  // query rows of the stage's tile
       const bool idle = quarter * 32 >= valid;             // none in this warp
       // the stage's record row (with one query tile, stage 1's is scratch behind
-      // it, within the rows that are the CTA's at this point)
-      float* mine = P.W.rec + (s.rec + st * 128 + r) * D;
+      // the records, within the rows that are the CTA's at this point)
+      const int behind = two ? 128 : s.rows;
+      float* mine = P.W.rec + (s.rec + st * behind + r) * D;
       float m = -INFINITY, l = 0.0f;
       // Before its first scores can be there, a warp runs a step on whatever its
       // TMEM holds, without storing, waiting or signalling: the instructions are
@@ -643,8 +644,8 @@ __global__ void __launch_bounds__(PrefixTcShape<D>::THREADS, 1)
               ld_global_v8(rec + 8, o[1]);
             }
             if (merge && steps1 > kFlush) {
-              ld_global_v8(rec + 128 * D, e[0]);
-              ld_global_v8(rec + 128 * D + 8, e[1]);
+              ld_global_v8(rec + behind * D, e[0]);
+              ld_global_v8(rec + behind * D + 8, e[1]);
             }
 #pragma unroll
             for (int j = 0; j < 16; j++) {

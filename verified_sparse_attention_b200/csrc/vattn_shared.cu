@@ -117,23 +117,34 @@ size_t shared_workspace(vattn_ctx* ctx, char* p) {
   const vattn_config& c = ctx->cfg;
   const SharedKernels k = pick(ctx);
   const size_t B = static_cast<size_t>(c.max_batch);
-  // every block's rows once, and one block's rows per CTA for segments that a
-  // CTA's end cuts
-  const size_t rows = static_cast<size_t>(ctx->num_sms) * k.RB + B * c.num_q_heads;
+  // every block's rows once, and per CTA the most that a block takes (a single
+  // query tile of the tensor-core kernel twice: its second stage's scratch), for
+  // segments that a CTA's end cuts. A single sequence shares nothing.
+  const size_t most = B * ctx->G;  // query rows of a group
+  const int stride = static_cast<int>(std::min<size_t>(k.RB, k.tc ? 2 * most : most));
+  const size_t rows = B > 1 ? static_cast<size_t>(ctx->num_sms) * stride + B * c.num_q_heads : 0;
   const size_t sz_int = align256(B * sizeof(int)), sz_group = align256((B + 1) * sizeof(SharedGroup));
   const size_t sz_pre = align256((B + 1) * sizeof(int));
   const size_t sz_rec = align256(rows * c.head_dim * sizeof(float)), sz_ml = align256(rows * sizeof(float2));
   const int own_warps = k.own ? k.own_nw * ctx->num_sms : 0;
   // over the KV heads at most kOwnPieces pieces per warp, and one more per
-  // sequence and head
-  const size_t pieces = k.own ? static_cast<size_t>(vattn::kOwnPieces) * own_warps / c.num_kv_heads + B + 1 : 0;
-  const size_t own_rows = pieces * c.num_q_heads, sz_piece = align256(pieces * sizeof(OwnPiece));
+  // sequence and head; of a sequence at most as many as its chunks make (of
+  // max_ctx positions that begin inside a chunk). Every warp reads the entry of
+  // its index before it knows how many there are.
+  const size_t chunks = (static_cast<size_t>(c.max_ctx) + vattn::kOwnChunk - 1) / vattn::kOwnChunk + 1;
+  const size_t pieces =
+      k.own ? std::min(static_cast<size_t>(vattn::kOwnPieces) * own_warps / c.num_kv_heads + B + 1,
+                       B * ((chunks + vattn::kOwnPiece - 1) / vattn::kOwnPiece))
+            : 0;
+  const size_t entries = k.own ? std::max(pieces, static_cast<size_t>(own_warps) / c.num_kv_heads + 1) : 0;
+  const size_t own_rows = pieces * c.num_q_heads, sz_piece = align256(entries * sizeof(OwnPiece));
   const size_t sz_orec = align256(own_rows * c.head_dim * sizeof(float)), sz_oml = align256(own_rows * sizeof(float2));
   if (p) {
     SharedWork& w = ctx->shared;
     w.reach = reinterpret_cast<int*>(p); p += 2 * sz_int;
     w.pages_ok = reinterpret_cast<int*>(p); p += sz_int;
     w.group = reinterpret_cast<SharedGroup*>(p); p += sz_group;
+    w.stride = stride;
     w.rec = reinterpret_cast<float*>(p); p += sz_rec;
     w.ml = reinterpret_cast<float2*>(p); p += sz_ml;
     w.own_pre = reinterpret_cast<int*>(p); p += sz_pre;

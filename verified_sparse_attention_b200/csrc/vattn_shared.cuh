@@ -422,7 +422,7 @@ __device__ __forceinline__ Segment segment_at(const SharedParams& P, const Share
   s.next = x + (s.t1 - s.t0);
   s.row0 = s.mb * P.RB;
   s.rows = min(P.RB, g.size * P.D.G - s.row0);
-  s.rec = static_cast<long long>(blockIdx.x) * P.RB + g.row0 + block_row0(P, s.mb, s.h, s.rows);
+  s.rec = static_cast<long long>(blockIdx.x) * P.W.stride + g.row0 + block_row0(P, s.mb, s.h, s.rows);
   return s;
 }
 // Group of flattened tile x (every warp by itself).
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(kSharedCombWarps * 32) k_shared_combine(const 
     float rm = -INFINITY, rl = 0.0f;
     const float* src = nullptr;
     if (j < np) {
-      const long long row = static_cast<long long>(slice_rec(pre, Tp, C, j)) * P.RB + base;
+      const long long row = static_cast<long long>(slice_rec(pre, Tp, C, j)) * P.W.stride + base;
       const float2 v = P.W.ml[row];
       rm = v.x;
       rl = v.y;
