@@ -91,6 +91,29 @@ def test_rotate_wrapper_refuses_host_tensors_and_shapes():
             r.rotate(bad, pos)
 
 
+def test_rotate_refuses_what_autograd_would_have_to_follow():
+    r = Rotary(head_dim=64)
+    x = torch.zeros(3, 2, 64, requires_grad=True)
+    pos = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="gradient"):
+        r.rotate(x, pos)
+    with pytest.raises(ValueError, match="gradient"):
+        r.rotate(x * 2, pos, out=torch.zeros(3, 2, 64))
+    for call in (lambda: r.rotate(x.detach(), pos), torch.no_grad()(lambda: r.rotate(x, pos))):
+        with pytest.raises(ValueError, match="CUDA device"):    # a host tensor is all that is wrong with it
+            call()
+
+
+@pytest.mark.gpu
+def test_rotate_takes_leaves_without_autograd():
+    r = Rotary(head_dim=64)
+    x = torch.randn(3, 2, 64, device="cuda", requires_grad=True)
+    pos = torch.arange(3, dtype=torch.int32, device="cuda")
+    with torch.no_grad():
+        got = r.rotate(x, pos)
+    assert not got.requires_grad and torch.equal(got, r.rotate(x.detach(), pos))
+
+
 # ------------------------------------------------------------ on the GPU
 # fp32: cos and sin to 2^-22 (angle 2^-32 turns + 2^-25 relative, sincospif, the amplitude's product), two
 # products and a sum of half an ulp each: |err| <= 2^-21 (|a| + |b|) A. bf16 adds half an ulp of the result.

@@ -41,9 +41,13 @@ class Rotary:
 
         x may be strided over tokens and heads. out: a tensor like x (x itself to
         rotate in place); new and contiguous by default. transpose: the transposed
-        rotation, which turns the gradient of the result into that of x; autograd
-        does not record the call.
+        rotation, which turns the gradient of the result into that of x. Autograd
+        neither records the call nor sees that out was written; an x that it would
+        have to follow is refused (pass x.detach(), or call under torch.no_grad()).
         """
+        if x.requires_grad and torch.is_grad_enabled():
+            raise ValueError("x requires a gradient, and autograd does not record this call: pass x.detach() and rotate "
+                             "the result's gradient with transpose=True")
         shape, strides, index = x.shape, x.stride(), x.get_device()
         dtype = _DTYPES.get(x.dtype)
         if len(shape) != 3 or shape[2] != self.head_dim or strides[2] != 1 or dtype is None or index < 0:
