@@ -362,7 +362,7 @@ int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const void* k_cache
                               const int32_t* prefix_lens, int groups, int batch, int num_pages,
                               float* out, void* stream);
 
-/* sync != 0: wait for the device, then return and clear the device error
+/* sync != 0: wait for the context's device, then return and clear the device error
    word (VATTN_DEV_* bits). sync == 0: return the host status of the last
    call on this context, without touching the device. */
 int vattn_last_error(vattn_ctx* ctx, int sync);

@@ -313,6 +313,8 @@ int vattn_score_pass_ms(vattn_ctx* ctx, double* total_ms, int* count, int reset)
 int vattn_last_error(vattn_ctx* ctx, int sync) {
   if (!ctx) return VATTN_EINVAL;
   if (!sync) return ctx->last_status;
+  vattn::DeviceScope scope(ctx->device);  // the context's calls run there, whichever device is current
+  if (!scope.ok) return VATTN_ECUDA;
   if (cudaDeviceSynchronize() != cudaSuccess) return VATTN_ECUDA;
   unsigned v = 0;
   if (cudaMemcpy(&v, ctx->err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return VATTN_ECUDA;
