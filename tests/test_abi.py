@@ -74,6 +74,26 @@ def test_binding_struct_offsets_match_the_compiled_header(tmp_path):
             assert got[(struct, name)] == getattr(cls, name).offset, (struct, name)
 
 
+def test_binding_of_the_rotary_and_append_structs_matches_the_compiled_header(tmp_path):
+    fields = {"vattn_rope_config": _abi.vattn_rope_config, "vattn_rope": _abi.vattn_rope,
+              "vattn_append_params": _abi.vattn_append_params}
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "vattn.h"', "int main(void) {"]
+    for struct, cls in fields.items():
+        lines.append(f'  printf("{struct} size %zu\\n", sizeof({struct}));')
+        for name, _ in cls._fields_:
+            lines.append(f'  printf("{struct} {name} %zu\\n", offsetof({struct}, {name}));')
+    lines += ["  return 0;", "}"]
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(lines) + "\n")
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), "-o", str(exe), str(src)], check=True)
+    got = dict(line.rsplit(" ", 1) for line in
+               subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines())
+    for struct, cls in fields.items():
+        assert int(got[f"{struct} size"]) == C.sizeof(cls), struct
+        for name, _ in cls._fields_:
+            assert int(got[f"{struct} {name}"]) == getattr(cls, name).offset, (struct, name)
+
+
 def test_strerror_without_device(lib):
     _abi.lib()
     assert _abi.vattn_strerror(_abi.VATTN_EINVAL) == "invalid argument"
