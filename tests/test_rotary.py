@@ -230,7 +230,7 @@ def test_rotate_failure_leaves_nothing_for_the_next_call():
     x = torch.randn(5, 4, 64, device="cuda").bfloat16()
     pos = torch.arange(5, dtype=torch.int32, device="cuda")
     r = Rotary(head_dim=64)
-    ref = r.rotate(x, pos)
+    ref, out = r.rotate(x, pos), torch.empty_like(x)
     dec = SparseDecoder(num_q_heads=4, num_kv_heads=4, head_dim=64, dtype=torch.bfloat16, page_size=16, max_batch=1,
                         max_ctx=16)
     cache = torch.randn(1, 4, 16, 64, device="cuda").bfloat16()
@@ -242,7 +242,7 @@ def test_rotate_failure_leaves_nothing_for_the_next_call():
     try:
         assert rt.cudaStreamSynchronize(stream) != 0
         with pytest.raises(_abi.VattnError):
-            r.rotate(x, pos, stream=stream.value)
+            r.rotate(x, pos, out=out, stream=stream.value)
     finally:
         rt.cudaStreamEndCapture(stream, C.byref(graph))
         rt.cudaGetLastError()

@@ -601,6 +601,37 @@ def test_shared_accumulators_of_many_steps_lose_nothing_more():
     dec.close()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_new_outputs_of_another_stream_leave_the_current_ones_memory(handle):
+    # memory that the current stream has freed, and still reads, is not what a call on another stream writes to
+    x = shared_batch([64], [600], [b for b in range(64)], Hq=32, Hkv=8, d=128, ps=16, dtype=torch.float32)
+    dec = _decoder(x, "f32", 16)
+    y = _cuda(x)
+    r = Rotary(head_dim=128)
+    other = torch.cuda.Stream()
+    stream = other.cuda_stream if handle else other
+    one = torch.arange(64, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(64, 8, 128, device="cuda") for _ in range(2))
+    spare = {n: torch.zeros_like(y[n]) for n in ("k_cache", "v_cache")}
+    calls = [lambda **kw: r.rotate(y["q"], one, **kw), lambda **kw: _call(dec, y, **kw),
+             lambda **kw: dec.append(k, v, spare["k_cache"], spare["v_cache"], y["page_table"], y["seq_lens"],
+                                     x["num_pages"], rotary=r, q=y["q"], **kw)]
+    for call in calls:
+        want = call().clone()
+        torch.cuda.synchronize()
+        held = torch.full_like(want, 3.0)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)           # 10 ms of the current stream
+        seen = held * 2
+        del held
+        got = call(stream=stream)
+        torch.cuda.synchronize()
+        assert (seen == 6).all() and torch.equal(got, want)
+        del got, seen
+    dec.close()
+
+
 # ------------------------------------------------------------ as they are used together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -140,6 +140,18 @@ def _stream_ptr(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def empty_for(stream, *args, **kw):
+    """torch.empty for a call on `stream` (None: the current one): memory that the allocator keeps for that
+    stream, so that the call need not wait for what another stream still does with it."""
+    import torch
+    if stream is None:
+        return torch.empty(*args, **kw)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=kw["device"])
+    with torch.cuda.stream(stream):
+        return torch.empty(*args, **kw)
+
+
 def vattn_create(config):
     """Create a context from a vattn_config (or a dict of its fields); returns the handle."""
     if isinstance(config, dict):

@@ -135,7 +135,8 @@ class SparseDecoder:
         if q is not None:
             p.q_stride = self._check_rows("q", q, tokens, self.num_q_heads)
             if q_out is None:
-                q_out = torch.empty((tokens, self.num_q_heads, self.head_dim), dtype=self.dtype, device=self.device)
+                q_out = _abi.empty_for(stream, (tokens, self.num_q_heads, self.head_dim), dtype=self.dtype,
+                                       device=self.device)
             elif self._check_rows("q_out", q_out, tokens, self.num_q_heads) != self.num_q_heads * self.head_dim:
                 raise ValueError("q_out must be contiguous")
             p.q, p.q_out = q.data_ptr(), q_out.data_ptr()
@@ -184,7 +185,8 @@ class SparseDecoder:
         self._check_index("prefix_lens", prefix_lens, (groups,))
         self._check_index("group_start", group_start, (groups + 1,))
         if out is None:
-            out = torch.empty((batch, self.num_q_heads, self.head_dim), dtype=torch.float32, device=self.device)
+            out = _abi.empty_for(stream, (batch, self.num_q_heads, self.head_dim), dtype=torch.float32,
+                                 device=self.device)
         elif out.dtype is not torch.float32 or out.shape != q.shape or not out.is_contiguous() \
                 or out.get_device() != self._index:
             raise ValueError(f"out must be contiguous float32 {list(q.shape)} on {self.device}")

@@ -58,7 +58,7 @@ class Rotary:
                 or positions.get_device() != index:
             raise ValueError("positions must be contiguous int32 [tokens] on x's device")
         if out is None:
-            out = torch.empty((tokens, heads, self.head_dim), dtype=x.dtype, device=x.device)
+            out = _abi.empty_for(stream, (tokens, heads, self.head_dim), dtype=x.dtype, device=x.device)
         elif out.shape != shape or out.dtype is not x.dtype or out.get_device() != index or out.stride(2) != 1:
             raise ValueError("out must be like x")
         if stream is None:
