@@ -365,8 +365,9 @@ __device__ __forceinline__ unsigned pack2(float lo, float hi) {
 
 // Projected keys of a tile of bf16 keys: [TT tokens x D] . [D x 32] on the
 // tensor cores, the fp32 basis as three bf16 terms, which hold its 24 bits whole:
-// the products are exact and summed in fp32. (Two terms lose 2^-17 of a basis
-// entry; that moved one bf16 result in 400 to its neighbour.) The block splits
+// the products are exact and summed in fp32: 134 of 2.1 million bf16 results are
+// not the 64-bit product rounded, 325 of an fp32 matrix product. (Two terms lose
+// 2^-17 of a basis entry; that moved one result in 400.) The block splits
 // a head's basis once per job into shared memory; every warp has 16 tokens and
 // 4 TT / 16 components. 8190 tokens of 8 heads (71 MB): 26.2 us (two terms: 25.2), of which 6 us
 // go without the projection and 3 without the cosines (each warp splitting its
@@ -417,11 +418,13 @@ __device__ __forceinline__ void project_tile(const __nv_bfloat16* s_key, const u
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int m0 = 16 * (warp % MT), n0 = 8 * NX * (warp / MT);
   if (m0 >= n) return;
-  float acc[NX][4];
+  // The tensor core truncates what it adds, by the accumulator's magnitude: the
+  // second and third terms have one of their own.
+  float acc[NX][4], small[NX][4];
 #pragma unroll
   for (int x = 0; x < NX; x++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) acc[x][i] = 0.0f;
+    for (int i = 0; i < 4; i++) acc[x][i] = small[x][i] = 0.0f;
   const unsigned rows = smem_addr(s_key + (m0 + (lane & 15)) * LD + (lane >> 4) * 8);
   // lanes 0-15 address the first term of 16 rows, lanes 16-31 the second
   const unsigned brow = smem_addr(s_basis + (lane & 15) * 128);
@@ -441,11 +444,15 @@ __device__ __forceinline__ void project_tile(const __nv_bfloat16* s_key, const u
         unsigned b[4];
         ldsm4_t(brow + (k + 16 * i) * 128 + (((2 * (n0 / 8 + x) + (lane >> 4)) ^ (lane & 7)) << 4), b);
         mma16816(acc[x], a[i], b[0], b[1]);
-        mma16816(acc[x], a[i], b[2], b[3]);
-        mma16816(acc[x], a[i], c[2 * i], c[2 * i + 1]);
+        mma16816(small[x], a[i], b[2], b[3]);
+        mma16816(small[x], a[i], c[2 * i], c[2 * i + 1]);
       }
     }
   }
+#pragma unroll
+  for (int x = 0; x < NX; x++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) acc[x][i] += small[x][i];
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.k_proj);
 #pragma unroll
   for (int half = 0; half < 2; half++) {
