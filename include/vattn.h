@@ -297,7 +297,7 @@ int vattn_rotate(const vattn_rope* rope, const void* x, void* out, const int32_t
  * sequence of length 0 appends nothing.
  * Per token: k_cache gets the key rotated by `rope`, v_cache the value; a
  * SparQ context's k_t_cache the same key dim-major; a Loki context's
- * k_proj_cache the stored (rounded) key times the basis, summed in fp32; q_out
+ * k_proj_cache the stored (rounded) key times the fp32 basis, summed in fp32; q_out
  * the rotated query. Nothing else of the caches or of q_out is written: rows
  * from cu_tokens[batch] on are left alone.
  * Slots must differ: two tokens with one slot (a page listed twice) race.
@@ -335,7 +335,9 @@ int vattn_append(vattn_ctx* ctx, const vattn_append_params* params, const int32_
 
 /* ------------------------------------------------------------------------
  * Dense decode for a batch that shares prefixes: vattn_dense_decode's result,
- * with every shared prefix's keys and values read once per group of sequences.
+ * with a shared prefix's keys and values read once for all sequences of a group
+ * that reach its end, where there are two or more of them (fp32 caches in device
+ * memory: 5, 4 or 3 with Hq / Hkv up to 2, 4 or 8; fewer read it once each).
  *   groups       at least 1, at most max_batch
  *   group_start  [groups + 1] device int32, ascending from 0 to batch: group g
  *                is sequences group_start[g] .. group_start[g + 1] - 1
@@ -352,6 +354,10 @@ int vattn_append(vattn_ctx* ctx, const vattn_append_params* params, const int32_
  * sequences of such a group, and those in no group, give a zero output. A page
  * out of range sets VATTN_DEV_BAD_PAGE: the sequences that would read it give a
  * zero output.
+ * Scores, softmax statistics and sums are fp32. With bf16 caches in device memory
+ * the weights are two bf16 terms (2^-16 of a weight) and the tensor core truncates
+ * its fp32 sums (up to 7e-6 of an output): about 5e-6 of a row's norm in all on
+ * random values; other caches are multiplied in fp32 throughout.
  * q and the caches start at multiples of 16 bytes, the other arrays at multiples of
  * their element's size (else VATTN_EINVAL).
  * Uses the context's workspace like the other decodes: order the calls of one

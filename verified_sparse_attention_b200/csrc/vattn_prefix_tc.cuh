@@ -24,17 +24,17 @@
 //   warp 10         lets the next kernel start
 // TMEM (512 columns): S0, S1, O0, O1 of 128 each. The weights of 32 keys
 // overwrite their scores as two bf16 terms (hi = bf16(p), lo = bf16(p - hi),
-// 2^-17 relative; 16 columns each), the A operand of two products with V: the
-// outputs are fp32, and one term would leave 2^-9. The running maximum moves only when a tile exceeds it by more
-// than 2^8 (weights stay below 2^8, far inside fp32 and bf16), so O is rarely
-// rescaled; by the time a tile's scores are read, the stage's previous product
+// 2^-16 relative; 16 columns each), the A operand of two products with V: the
+// outputs are fp32, and one term would leave 2^-8. The running maximum moves only
+// when a tile exceeds it by more than 2^8 (weights stay below 2^8, far inside
+// fp32 and bf16), so O is rarely rescaled; by the time a tile's scores are read, the stage's previous product
 // is complete (both are issued in order), so the softmax threads may rescale O.
 //
 // d = 128, 8 KV heads, 4 query heads each. 32 sequences over 32768 keys (one
 // query tile): 134 MB in about 36 us of a 62 us call, bound by HBM (5.5 TB/s
 // between the first tile and the records, 3.5 TB/s with them). 256 sequences
 // over 8192 keys (two tiles, four blocks per head): 52 GFLOP with both terms in
-// about 45 us of a 98 us call, 1.2 PFLOP/s with the tensor pipe active half the
+// about 45 us of a 99 us call, 1.2 PFLOP/s with the tensor pipe active half the
 // time: bound by the chain scores, softmax, weights, product of each stage.
 // Without the second term's products it takes 3 us less, without the
 // exponentials 2 us, so neither bounds it by itself. Two softmax threads per row

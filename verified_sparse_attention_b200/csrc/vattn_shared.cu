@@ -210,7 +210,7 @@ extern "C" int vattn_shared_dense_decode(vattn_ctx* ctx, const void* q, const vo
   // link every byte counts: two sequences are enough. The fp32 kernel takes as
   // long as the gather takes for 4.7, 3.7 and 2.2 sequences with 1, 4 and 8
   // query heads per KV head (16384 keys x 8 heads, d = 128: 91 to 94 us against
-  // 19.5, 24.5 and 41 us a sequence).
+  // 19.5, 24.5 and 41 us a sequence; both grow with the keys).
   P.min_reach = k.tc || P.D.kv_host ? 2 : ctx->G < 4 ? 5 : ctx->G < 8 ? 4 : 3;
   if (!k.own && !P.D.kv_host)
     if (const int rc = vattn::encode_row_maps(c, k_cache, v_cache, num_pages, &P.D)) return ctx->last_status = rc;

@@ -123,7 +123,8 @@ class SparseDecoder:
         [batch + 1]: the tokens of sequence b are cu_tokens[b] .. cu_tokens[b+1]-1; None:
         one token per sequence (none where the length is 0). A SparQ context also takes
         k_t_cache, a Loki context k_proj_cache and proj_basis. Returns q_out, new and
-        contiguous by default (None without q); see vattn_append in include/vattn.h.
+        contiguous by default (None without q). Autograd records nothing of the call;
+        see vattn_append in include/vattn.h.
         """
         batch = self._check_caches(k_cache, v_cache, page_table, seq_lens, num_pages)
         tokens = k.shape[0]
