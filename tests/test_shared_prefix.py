@@ -632,6 +632,26 @@ def test_new_outputs_of_another_stream_leave_the_current_ones_memory(handle):
     dec.close()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("groups", [20, 1100])
+def test_shared_many_groups_behind_short_first_sequences(dtype, groups):
+    # in every group one of two sequences reaches the prefix's end, mostly the second, which does not list its pages
+    prefixes = [20 + g % 40 for g in range(groups)]
+    own = [v for g in range(groups) for v in ((-3, g % 7) if g % 3 else (g % 5, -4))]
+    x = shared_batch([2] * groups, prefixes, own, Hq=4, Hkv=2, d=64, ps=16, dtype=DT[dtype], seed=15)
+    ref = dense64(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["seq_lens"])
+    table = x["page_table"].clone()
+    for g in range(groups):
+        if g % 3:
+            table[2 * g + 1, :prefixes[g] // 16] = -1
+    dec = _decoder(x, dtype, 16)
+    got = _call(dec, _cuda(dict(x, page_table=table))).cpu().double()
+    assert dec.last_error() == 0
+    assert float(_row_errors(got, ref).max()) <= ROW_TOL
+    dec.close()
+
+
 # ------------------------------------------------------------ as they are used together
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
