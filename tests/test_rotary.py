@@ -250,3 +250,17 @@ def test_rotate_failure_leaves_nothing_for_the_next_call():
     dec.dense(x[:1], cache, cache, table, lens, 1)       # reported the failure of the rotation
     assert dec.last_error() == 0 and torch.equal(r.rotate(x, pos), ref)
     dec.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("stream", [0, 1, 2])
+def test_rotate_takes_the_default_streams_handles(stream):
+    # the legacy default stream's two and the thread's own
+    r = Rotary(head_dim=64)
+    x = torch.randn(7, 3, 64, device="cuda")
+    pos = torch.arange(7, dtype=torch.int32, device="cuda")
+    want = r.rotate(x, pos)
+    torch.cuda.synchronize()
+    got = r.rotate(x, pos, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

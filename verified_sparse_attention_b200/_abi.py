@@ -146,8 +146,9 @@ def empty_for(stream, *args, **kw):
     import torch
     if stream is None:
         return torch.empty(*args, **kw)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=kw["device"])
+    if isinstance(stream, int):  # 0 and 1 are the legacy default stream's handles
+        stream = (torch.cuda.default_stream(kw["device"]) if stream in (0, 1) else
+                  torch.cuda.ExternalStream(stream, device=kw["device"]))
     with torch.cuda.stream(stream):
         return torch.empty(*args, **kw)
 
