@@ -346,8 +346,9 @@ int vattn_append(vattn_ctx* ctx, const vattn_append_params* params, const int32_
  *                sequence of the group. They are read through the page table of
  *                the group's first sequence (which has to list them even if that
  *                sequence itself is shorter), the rest through each
- *                sequence's own, whose entries and rows for the prefix's
- *                positions may hold anything. The prefix need not end on a page.
+ *                sequence's own. Entries and rows of the others for the prefix's
+ *                positions may hold anything, where they reach its end. The
+ *                prefix need not end on a page.
  * A sequence shorter than its group's prefix is decoded by itself from its own
  * pages. An empty sequence gives a zero output. Invalid groups (not ascending
  * from 0 to batch, a prefix outside [0, max_ctx]) set VATTN_DEV_BAD_GROUP: the
